@@ -697,6 +697,207 @@ PATCH_API patch_status_t patch_gemm64(const uint16_t *X, int64_t M, const patch_
 PATCH_API patch_status_t patch_mma_probe_m(int m, int sparse, int64_t iters, int32_t *dev_status, void *stream);
 
 /*
+ * ---- the decoder layer beside its linears: rotary positions, a paged 8-bit
+ * key/value cache and attention over it, and linears with 4-bit weights (the
+ * pages measure LLaMA-2 7B end to end, "Experimental Results" -> "Speedup &
+ * Efficiency"; these operators are LLaMA's layer and common practice around
+ * it, not stated by the pages).
+ *
+ * Element types of their inputs and outputs: */
+#define PATCH_DTYPE_BF16 0
+#define PATCH_DTYPE_FP16 1
+#define PATCH_DTYPE_FP32 2
+
+/* Rows of heads (host struct): element (token t, head h, d) is at
+ * data[t * token_stride + h * head_stride + d], strides in elements.  A slice
+ * of a fused q|k|v projection's rows is one.  data must be 16-byte aligned and
+ * both strides whole multiples of 16 bytes (strides of a size-1 axis do not
+ * matter). */
+typedef struct {
+    void *data;
+    int64_t heads, token_stride, head_stride;
+} patch_heads;
+
+/*
+ * patch_rope_table: rotary angles of the positions 0 .. n_pos - 1 as
+ * (cos, sin) pairs, table fp32 [n_pos][rot_dim / 2][2].  Pair i turns by
+ * pos * w_i, w_i = base^(-2i / rot_dim) scaled for long contexts:
+ *   PATCH_ROPE_PLAIN   as is;
+ *   PATCH_ROPE_LINEAR  w_i / factor (position interpolation);
+ *   PATCH_ROPE_BANDS   by wavelength l = 2 pi / w_i against c =
+ *       original_positions: w_i where l < c / high_freq, w_i / factor where
+ *       l > c / low_freq, and between them (1 - s) w_i / factor + s w_i with
+ *       s = (c / l - low_freq) / (high_freq - low_freq) (LLaMA-3's rule);
+ *   PATCH_ROPE_YARN    w_i (1 - r_i) + (w_i / factor) r_i, r_i the ramp from 0
+ *       to 1 between the pairs that turn high_freq (fast) and low_freq (slow)
+ *       times over original_positions (YaRN, arXiv 2309.00071).
+ * cos and sin are multiplied by amplitude (YaRN's attention factor; 1 = none).
+ * Angles, sines and cosines are computed in 64 bits and rounded once.
+ * Errors: PATCH_ERR_INVALID_ARG (NULL; base not > 1; unknown kind; factor,
+ * original_positions, low_freq or high_freq not positive and finite where the
+ * kind uses them; BANDS and YARN need low_freq < high_freq),
+ * PATCH_ERR_SHAPE (n_pos outside 1 .. 2^30, rot_dim not an even number in
+ * 2 .. 1024), PATCH_ERR_ALIGN (table not 16-byte aligned), PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ */
+#define PATCH_ROPE_PLAIN 0
+#define PATCH_ROPE_LINEAR 1
+#define PATCH_ROPE_BANDS 2
+#define PATCH_ROPE_YARN 3
+typedef struct {
+    int32_t kind;
+    int32_t reserved; /* set to 0 */
+    double base, factor, original_positions, low_freq, high_freq, amplitude;
+} patch_rope_config;
+PATCH_API patch_status_t patch_rope_table(int64_t n_pos, int64_t rot_dim, const patch_rope_config *config,
+                                          float *table, void *stream);
+
+/*
+ * patch_rope: rotary positions of query and key heads in one launch.  The
+ * first rot_dim elements of every head are rot_dim / 2 pairs (a, b), turned by
+ * their token's row of the table,
+ *     (a c - b s, b c + a s);
+ * the others are copied.  PATCH_ROPE_HALF pairs element i with i + rot_dim / 2,
+ * PATCH_ROPE_INTERLEAVED pairs 2i with 2i + 1.  backward != 0 applies the
+ * transpose (sines negated): the gradient of the inputs from the gradient of
+ * the outputs.  fp32 arithmetic, each product and sum rounded by itself, one
+ * rounding to the type.
+ *   q, k       inputs (k may be NULL), n_tokens rows each, dtype PATCH_DTYPE_*
+ *   q_out, k_out  outputs; may be the inputs (same data and strides: in
+ *              place), else they may not overlap them
+ *   positions  int32 [n_tokens] device, 0 .. n_pos - 1; a token with another
+ *              position is skipped (its output rows are not written) and, unless
+ *              it is -1 (padding), sets PATCH_DEV_BOUNDS
+ *   table      fp32 [n_pos][rot_dim / 2][2] device (patch_rope_table)
+ * dev_status may be NULL.
+ * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts of input and output that
+ * differ, unknown layout or dtype), PATCH_ERR_SHAPE (rot_dim not a multiple of 16 in
+ * 16 .. head_dim, head_dim not a multiple of 8 up to 1024, n_tokens > 2^30), PATCH_ERR_ALIGN,
+ * PATCH_ERR_DEVICE, PATCH_ERR_CUDA.  n_tokens == 0 is a no-op.
+ */
+#define PATCH_ROPE_HALF 0
+#define PATCH_ROPE_INTERLEAVED 1
+PATCH_API patch_status_t patch_rope(const patch_heads *q, const patch_heads *k, const patch_heads *q_out,
+                                    const patch_heads *k_out, int64_t n_tokens, int64_t head_dim, int dtype,
+                                    const int32_t *positions, const float *table, int64_t n_pos, int64_t rot_dim,
+                                    int layout, int backward, int32_t *dev_status, void *stream);
+
+/* A paged key/value cache in 8 bits (host struct of device pointers, owned by
+ * the caller): n_pages pages of `page` tokens; k and v e4m3
+ * [n_pages][kv_heads][page][head_dim], k_scale and v_scale fp32
+ * [n_pages][kv_heads]: one scale for each page and head, a power of two.  An
+ * element stands for value * scale.  page 16, 32, 64 or 128; head_dim 64 or
+ * 128; all four 16-byte aligned.  Sequence b's token p lies in page
+ * block_table[b][p / page] at offset p % page (block_table int32
+ * [batch][max_pages]).  Full pages may be shared between sequences; a page
+ * that is being appended to belongs to one. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t n_pages, kv_heads, page, head_dim;
+} patch_kv8_cache;
+
+/*
+ * patch_kv8_append: store the keys and values of new tokens, the keys with
+ * their rotary positions applied on the way.  Sequence b holds past_lens[b]
+ * tokens; rows cu_new[b] .. cu_new[b + 1] - 1 of k and v become its tokens
+ * past_lens[b], past_lens[b] + 1, ... (their positions).  cu_new NULL: one new
+ * token per sequence (n_tokens == batch).  Rows from cu_new[batch] on are not read.
+ *
+ * Scale of a page and head: the least 2^e, e in -100 .. 119, with every new
+ * finite |x| <= 448 * 2^e, and at least the page's present scale if it holds
+ * tokens before the first new one; those are then stored again under the larger
+ * scale (by a power of two: exact but for what falls below e4m3's smallest
+ * step).  A page filled from its start takes no notice of what it held.
+ * Stored is x / scale rounded to e4m3 (nearest even, once, from fp32);
+ * infinities are stored as +-448, NaN as NaN.  Nothing else of the cache is written.
+ *   k, v       n_tokens rows of cache->kv_heads heads, dtype bf16 or fp16
+ *   past_lens  int32 [batch], cu_new int32 [batch + 1] (cu_new[0] == 0, not decreasing), device
+ *   table, n_pos, rot_dim, layout  as patch_rope; table NULL (rot_dim 0): keys are stored as they are
+ * A token whose page lies outside the block table or the pool, or whose
+ * position lies outside the table, sets PATCH_DEV_BOUNDS; its page is not
+ * written.  dev_status may be NULL.  Two sequences must not append to one page.
+ * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts, dtype, layout, n_tokens != batch
+ * without cu_new), PATCH_ERR_SHAPE (page, head_dim, rot_dim not a multiple of 16 up to head_dim,
+ * counts out of range), PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ */
+PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_heads *v, int64_t n_tokens, int dtype,
+                                          const patch_kv8_cache *cache, const int32_t *block_table,
+                                          int64_t max_pages, const int32_t *past_lens, const int32_t *cu_new,
+                                          int64_t batch, const float *table, int64_t n_pos, int64_t rot_dim,
+                                          int layout, int32_t *dev_status, void *stream);
+
+/*
+ * patch_attn_kv8: attention of new tokens over the cache,
+ *     out = softmax(scale * q K^T + mask) V,
+ * query head h reading key/value head h / (q->heads / kv_heads).  Sequence b's
+ * queries are rows cu_q[b] .. cu_q[b + 1] - 1 (cu_q NULL: one each, n_tokens ==
+ * batch) and it holds kv_lens[b] tokens, the new ones included.  Query i of m
+ * stands at position p = kv_lens[b] - m + i; causal != 0 hides the tokens after
+ * p; window > 0 (causal only) also those before p - window + 1.  A query that
+ * sees no token gives out = 0 and lse = -inf.  Rows from cu_q[batch] on are
+ * left as they were.
+ * fp32 scores, softmax statistics and sums; q and the probabilities enter the
+ * tensor cores as fp16 (q divided by a power of two of its own row first, so
+ * that no finite value overflows).
+ *   q, out     n_tokens rows of heads (q->heads a multiple of kv_heads, at most
+ *              16 times), dtype bf16 or fp16; out may be q (same strides)
+ *   lse        fp32 [n_tokens][q->heads] or NULL: log sum exp of the scaled scores
+ *   workspace  patch_attn_kv8_workspace_size bytes, 16-byte aligned, zero
+ *              before its first use; every call that reports no timeout leaves
+ *              its counters zero again, so one serves any number of calls of any
+ *              sizes on one stream.  Calls that may run at the same time need one each.
+ * A page id outside the pool, or kv_lens[b] outside 0 .. max_pages * page, sets
+ * PATCH_DEV_BOUNDS (the tokens there read as zeros; the length is clamped).
+ * Bounded waits as patch_gemm (wait_limit_us, 0 = 2 s).  dev_status may be NULL.
+ * Errors: PATCH_ERR_INVALID_ARG, PATCH_ERR_SHAPE, PATCH_ERR_ALIGN,
+ * PATCH_ERR_WORKSPACE, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ */
+PATCH_API patch_status_t patch_attn_kv8_workspace_size(int64_t n_tokens, int64_t batch, int64_t q_heads,
+                                                       const patch_kv8_cache *cache, size_t *bytes);
+PATCH_API patch_status_t patch_attn_kv8(const patch_heads *q, int64_t n_tokens, int dtype,
+                                        const patch_kv8_cache *cache, const int32_t *block_table,
+                                        int64_t max_pages, const int32_t *kv_lens, const int32_t *cu_q,
+                                        int64_t batch, float scale, int causal, int64_t window,
+                                        const patch_heads *out, float *lse, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_status, void *stream,
+                                        uint64_t wait_limit_us);
+
+/* A linear weight in 4 bits (host struct of device pointers):
+ * W[n][k] = (code - 8) * scale[n][k / group], code 0 .. 15; codes u8 [N][K / 2],
+ * the even k in the low half of a byte; scales [N][K / group] of scale_dtype
+ * (PATCH_DTYPE_*).  group 32, 64 or 128, K a multiple of it; any N.  codes and
+ * scales 16-byte aligned.  A pruned (zero) weight is code 8 and stays exactly zero. */
+typedef struct {
+    int64_t N, K;
+    int32_t group, scale_dtype;
+    const void *codes, *scales;
+} patch_weight4;
+
+/*
+ * patch_quantize4: W (bf16, fp16 or fp32 [N][K]) to 4 bits, nearest code under
+ * a group's scale amax / 7 (rounded to scale_dtype before the codes are taken):
+ * code = 8 + clamp(round(w / scale), -8, 7), ties to even; a group of zeros has scale 0 and codes 8.
+ * amax runs over the finite weights; infinities saturate and NaN becomes code 8.
+ * N, K, group and scale_dtype are taken from *out, whose codes and scales it
+ * writes.  Errors: PATCH_ERR_INVALID_ARG, PATCH_ERR_SHAPE, PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ */
+PATCH_API patch_status_t patch_quantize4(const void *W, int dtype, const patch_weight4 *out, void *stream);
+
+/*
+ * patch_gemm4: Y = X * W^T for up to PATCH_DECODE_MAX_M tokens and a 4-bit
+ * weight: the decode product of a linear the tile mask leaves alone (a
+ * vocabulary head, small projections).  X [M][K] and Y [M][N] bf16 or fp16
+ * (16-byte aligned X), fp32 sums, one rounding.  No workspace; deterministic.
+ * Launched with programmatic dependent launch: it reads W before the previous
+ * kernel in the stream has completed, X only after.
+ * Errors: PATCH_ERR_INVALID_ARG (NULL, M outside 0 .. 16, group, dtypes),
+ * PATCH_ERR_SHAPE (N < 1, K not a positive multiple of group, either > 2^31 - 1),
+ * PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.  M == 0 is a no-op.
+ */
+PATCH_API patch_status_t patch_gemm4(const void *X, int64_t M, int dtype, const patch_weight4 *W, void *Y,
+                                     void *stream);
+
+/*
  * patch_read_status: synchronise `stream`, copy *dev_status to *host_bits and
  * return the first error it encodes (PATCH_ERR_TIMEOUT, then BOUNDS, then
  * BAD_PATTERN, then COUNT) or PATCH_OK.  host_bits may be NULL.

@@ -21,6 +21,8 @@ Entry points (same names as the C ABI):
     patch_gemm_group / Group (independent GEMMs of any token count in one prefill launch)
     64 x 64 execution tiles: patch_pack64_sizes, patch_exec_tiles64, patch_pack64 -> PackedWeight64,
     patch_gemm64_workspace_size, patch_gemm64; patch_mma_probe_m (M = 64 or 128 MMA rate)
+    the decoder layer beside its linears (decoder.py): patch_rope_table, patch_rope, patch_kv8_append /
+    patch_attn_kv8 on a KvCache8 (new_kv_cache8), patch_quantize4 -> Weight4, patch_gemm4
 Helpers of this binding: save_packed(weight, path) / load_packed(path) keep a
 packed weight in one .npz file (shape, sparse-tile count, the three blobs).
 """
@@ -111,6 +113,7 @@ def lib() -> ctypes.CDLL:
             "patch_gemm64": [P, I64, WP, P, P, SZ, P, P, ctypes.c_uint64],
             "patch_check_weight": [WP, P, P],
         }
+        sigs.update(signatures())
         for name, args in sigs.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -637,3 +640,8 @@ def patch_mma_probe_m(m: int, sparse: bool, iters: int, status: torch.Tensor | N
     status = new_status() if status is None else status
     _check(lib().patch_mma_probe_m(int(m), 1 if sparse else 0, iters, _dev(status, "status"), _stream(stream)),
            "patch_mma_probe_m")
+
+
+# the decoder layer beside its linears (imports the helpers above)
+from .decoder import (KvCache8, Weight4, new_kv_cache8, patch_attn_kv8, patch_attn_kv8_workspace_size,  # noqa: E402
+                      patch_gemm4, patch_kv8_append, patch_quantize4, patch_rope, patch_rope_table, signatures)

@@ -5,25 +5,14 @@
 #include <vector>
 
 #include "common.cuh"
+#include "host_checks.cuh"
 #include "kernels.cuh"
 
 namespace patch {
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool shape_ok(int64_t N, int64_t K) {
   return N > 0 && K > 0 && N % kTile == 0 && K % kTile == 0 && N <= (int64_t(1) << 31) &&
          K <= (int64_t(1) << 31);
-}
-
-// SM count of the current device; PATCH_ERR_DEVICE unless it is compute capability 10.x
-static patch_status_t device_sms(int* sms) {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PATCH_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return PATCH_ERR_CUDA;
-  if (major != 10) return PATCH_ERR_DEVICE;
-  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PATCH_ERR_CUDA;
-  return PATCH_OK;
 }
 
 static patch_status_t check_weight(const patch_weight* W) {
@@ -76,7 +65,7 @@ const char* patch_strerror(patch_status_t s) {
   switch (s) {
     case PATCH_OK: return "ok";
     case PATCH_ERR_INVALID_ARG: return "invalid argument";
-    case PATCH_ERR_SHAPE: return "N and K must be positive multiples of 128";
+    case PATCH_ERR_SHAPE: return "unsupported size (hybrid weights: N and K positive multiples of 128)";
     case PATCH_ERR_ALIGN: return "pointer not 16-byte aligned";
     case PATCH_ERR_DEVICE: return "current device is not an sm_100 (B200-class) GPU";
     case PATCH_ERR_CUDA: return "CUDA call failed";

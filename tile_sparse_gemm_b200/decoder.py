@@ -1,0 +1,373 @@
+"""The decoder layer beside its linears: rotary positions, a paged 8-bit
+key/value cache and attention over it, and linears with 4-bit weights.
+
+Thin binding over the C ABI (include/patch.h), like the rest of the package: it
+checks and marshals arguments, every step runs in the library's sm_100a
+kernels.  The calls run on the tensors' own device and on `stream` (default:
+that device's current stream), launch only libpatch kernels, allocate only the
+outputs they are not given, never synchronise and can be captured in a CUDA
+graph.  A device status word is optional: `status=new_status()` collects what
+the kernels report (patch_read_status).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import PatchError, _check, lib
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # PATCH_DTYPE_*
+LAYOUTS = {"half": 0, "interleaved": 1}                           # PATCH_ROPE_HALF / PATCH_ROPE_INTERLEAVED
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}  # PATCH_ROPE_*
+KV8_PAGES = (16, 32, 64, 128)
+KV8_HEAD_DIMS = (64, 128)
+GROUPS4 = (32, 64, 128)
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original_positions", "low_freq", "high_freq", "amplitude")]
+
+
+class _Cache8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int64) for n in ("n_pages", "kv_heads", "page", "head_dim")]
+
+
+class _Weight4(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+def signatures() -> dict:
+    """ctypes argument types of this module's entry points."""
+    P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    H, C, W = (ctypes.POINTER(t) for t in (_Heads, _Cache8, _Weight4))
+    return {
+        "patch_rope_table": [I64, I64, ctypes.POINTER(_RopeConfig), P, P],
+        "patch_rope": [H, H, H, H, I64, I64, I32, P, P, I64, I64, I32, I32, P, P],
+        "patch_kv8_append": [H, H, I64, I32, C, P, I64, P, P, I64, P, I64, I64, I32, P, P],
+        "patch_attn_kv8_workspace_size": [I64, I64, I64, C, ctypes.POINTER(SZ)],
+        "patch_attn_kv8": [H, I64, I32, C, P, I64, P, P, I64, ctypes.c_float, I32, I64, H, P, P, SZ, P, P,
+                           ctypes.c_uint64],
+        "patch_quantize4": [P, I32, W, P],
+        "patch_gemm4": [P, I64, I32, W, P, P],
+    }
+
+
+def _call(name: str, device: torch.device, stream, *args, tail=()):
+    """Run a C entry point with `device` current: name(*args, stream, *tail)."""
+    other = torch.cuda.current_device() != device.index
+    with torch.cuda.device(device) if other else contextlib.nullcontext():
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        _check(getattr(lib(), name)(*args, s.cuda_stream, *tail), name)
+
+
+def _tensor(t: torch.Tensor, name: str, device, dtype, shape=None, contiguous=True) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _dtype(t: torch.Tensor, name: str, allowed=(torch.bfloat16, torch.float16)) -> int:
+    if t.dtype not in allowed:
+        raise ValueError(f"{name} is {t.dtype}, expected one of {[str(d) for d in allowed]}")
+    return DTYPES[t.dtype]
+
+
+def _heads(t: torch.Tensor, name: str, device=None, dtype=None) -> _Heads:
+    """[T][H][D] rows of heads: any token and head strides, elements in a row."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim]")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return _Heads(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+
+
+def _status(status, device) -> int | None:
+    return None if status is None else _tensor(status, "status", device, torch.int32)
+
+
+# ---- rotary positions
+
+
+def patch_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original_positions: float = 0.0, low_freq: float = 1.0, high_freq: float | None = None,
+                     amplitude: float | None = None, device="cuda", stream=None) -> torch.Tensor:
+    """(cos, sin) of every position's angles, fp32 [n_pos][rot_dim // 2][2], from 64-bit angles.
+
+    scaling for long contexts: "plain", "linear" (positions divided by factor),
+    "bands" (by wavelength against original_positions: LLaMA-3's rule, low_freq 1
+    and high_freq 4 by default) or "yarn" (a ramp between the pairs that turn
+    low_freq, 1, and high_freq, 32, times; amplitude 0.1 ln(factor) + 1 by default)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r}, expected one of {list(ROPE_SCALINGS)}")
+    if high_freq is None:
+        high_freq = 32.0 if scaling == "yarn" else 4.0
+    if amplitude is None:
+        amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1.0 else 1.0
+    cfg = _RopeConfig(ROPE_SCALINGS[scaling], 0, base, factor, original_positions, low_freq, high_freq, amplitude)
+    if n_pos < 1 or rot_dim < 2:
+        raise PatchError(2, "patch_rope_table")
+    table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    _call("patch_rope_table", table.device, stream, n_pos, rot_dim, ctypes.byref(cfg), table.data_ptr())
+    return table
+
+
+def _table(table: torch.Tensor, device) -> tuple[int, int, int]:
+    p = _tensor(table, "table", device, torch.float32)
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table must be [n_pos][rot_dim // 2][2] (patch_rope_table)")
+    return p, table.shape[0], 2 * table.shape[1]
+
+
+def _layout(layout: str) -> int:
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout {layout!r}, expected one of {list(LAYOUTS)}")
+    return LAYOUTS[layout]
+
+
+def patch_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor,
+               layout: str = "half", backward: bool = False, q_out: torch.Tensor | None = None,
+               k_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Rotary positions of q [T][H][D] and k [T][Hk][D] (or None) in one launch: (q_out, k_out).
+
+    bf16, fp16 or fp32; any token and head strides (slices of a fused q|k|v
+    projection).  The first 2 * table.shape[1] elements of each head turn, the
+    rest is copied.  positions int32 [T]; a token at -1 (padding) is skipped.
+    backward=True turns the other way (times the table's amplitude): the
+    gradient of the inputs from the gradient of the outputs.  Pass
+    q_out=q, k_out=k to work in place."""
+    dev = q.device
+    hq = _heads(q, "q")
+    dt = _dtype(q, "q", tuple(DTYPES))
+    T, _, D = q.shape
+    tab, n_pos, rot = _table(table, dev)
+    pos = _tensor(positions, "positions", dev, torch.int32, (T,))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    ho = _heads(q_out, "q_out", dev, q.dtype)
+    hk = hko = None
+    if k is not None:
+        hk = _heads(k, "k", dev, q.dtype)
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        elif k_out.shape != k.shape:
+            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        hko = _heads(k_out, "k_out", dev, q.dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    ref = ctypes.byref
+    _call("patch_rope", dev, stream, ref(hq), ref(hk) if hk else None, ref(ho), ref(hko) if hko else None, T, D, dt,
+          pos, tab, n_pos, rot, _layout(layout), 1 if backward else 0, _status(status, dev))
+    return q_out, k_out
+
+
+# ---- the paged 8-bit cache
+
+
+@dataclass
+class KvCache8:
+    """A paged key/value cache in 8 bits: e4m3 pages [n_pages][kv_heads][page][head_dim] and
+    one power-of-two scale per page and head, fp32 [n_pages][kv_heads], for keys and for values."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def struct(self) -> _Cache8:
+        k, s = self.k, self.k_scale
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("cache.k must be [n_pages][kv_heads][page][head_dim]")
+        n, h, page, d = k.shape
+        f8, dev = torch.float8_e4m3fn, k.device
+        return _Cache8(_tensor(k, "cache.k", dev, f8), _tensor(self.v, "cache.v", dev, f8, k.shape),
+                       _tensor(s, "cache.k_scale", dev, torch.float32, (n, h)),
+                       _tensor(self.v_scale, "cache.v_scale", dev, torch.float32, (n, h)), n, h, page, d)
+
+    @property
+    def stored_bytes(self) -> int:
+        return 2 * self.k.numel() + 8 * self.k_scale.numel()
+
+
+def new_kv_cache8(n_pages: int, kv_heads: int, page: int, head_dim: int, device="cuda") -> KvCache8:
+    """An empty cache of n_pages pages of `page` tokens."""
+    if page not in KV8_PAGES or head_dim not in KV8_HEAD_DIMS:
+        raise ValueError(f"page {page} (expected {KV8_PAGES}) or head_dim {head_dim} (expected {KV8_HEAD_DIMS})")
+    k, v = (torch.zeros((n_pages, kv_heads, page, head_dim), dtype=torch.float8_e4m3fn, device=device)
+            for _ in range(2))
+    return KvCache8(k, v, *(torch.zeros((n_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _block_table(block_table: torch.Tensor, device) -> tuple[int, int, int]:
+    p = _tensor(block_table, "block_table", device, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_pages]")
+    return p, block_table.shape[0], block_table.shape[1]
+
+
+def patch_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache8, block_table: torch.Tensor,
+                     past_lens: torch.Tensor, cu_new: torch.Tensor | None = None, table: torch.Tensor | None = None,
+                     layout: str = "half", status: torch.Tensor | None = None, stream=None) -> None:
+    """Store new tokens' keys and values (bf16 or fp16 [T][Hk][D], any token and head strides) in the cache.
+
+    Sequence b holds past_lens[b] tokens (int32) and gets rows cu_new[b] ..
+    cu_new[b + 1] - 1 (int32 [batch + 1]; None: one token each) at the positions
+    that follow, in the pages of block_table (int32 [batch][max_pages]).  With a
+    table (patch_rope_table) the keys are rotated to their positions on the way."""
+    dev = cache.k.device
+    c = cache.struct()
+    hk = _heads(k, "k", dev)
+    hv = _heads(v, "v", dev, k.dtype)
+    dt = _dtype(k, "k")
+    if k.shape != v.shape or k.shape[1:] != (c.kv_heads, c.head_dim):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}, expected [tokens][{c.kv_heads}][{c.head_dim}]")
+    bt, batch, max_pages = _block_table(block_table, dev)
+    past = _tensor(past_lens, "past_lens", dev, torch.int32, (batch,))
+    cu = None if cu_new is None else _tensor(cu_new, "cu_new", dev, torch.int32, (batch + 1,))
+    tab, n_pos, rot = (None, 0, 0) if table is None else _table(table, dev)
+    ref = ctypes.byref
+    _call("patch_kv8_append", dev, stream, ref(hk), ref(hv), k.shape[0], dt, ref(c), bt, max_pages, past, cu, batch,
+          tab, n_pos, rot, _layout(layout), _status(status, dev))
+
+
+def patch_attn_kv8_workspace_size(n_tokens: int, batch: int, q_heads: int, cache: KvCache8) -> int:
+    b, c = ctypes.c_size_t(), cache.struct()
+    with torch.cuda.device(cache.k.device):
+        _check(lib().patch_attn_kv8_workspace_size(n_tokens, batch, q_heads, ctypes.byref(c), ctypes.byref(b)),
+               "patch_attn_kv8_workspace_size")
+    return b.value
+
+
+def patch_attn_kv8(q: torch.Tensor, cache: KvCache8, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                   cu_q: torch.Tensor | None = None, scale: float | None = None, causal: bool = True, window: int = 0,
+                   out: torch.Tensor | None = None, want_lse: bool = False, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, wait_limit_us: int = 0, stream=None):
+    """Attention of q (bf16 or fp16 [T][H][D]) over the cache: out, or (out, lse fp32 [T][H]) with want_lse.
+
+    Sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 (None: one each)
+    and it holds kv_lens[b] tokens, its new ones included (int32 both).  causal:
+    a query sees the tokens up to its own position; window > 0: only the last
+    `window` of them.  A query that sees none gives zeros and lse -inf.  scale
+    defaults to 1 / sqrt(D).  workspace: patch_attn_kv8_workspace_size bytes
+    (uint8), zero-filled once, reusable by any later call on the same stream."""
+    dev = cache.k.device
+    c = cache.struct()
+    hq = _heads(q, "q", dev)
+    dt = _dtype(q, "q")
+    T, H, D = q.shape
+    if D != c.head_dim or H % c.kv_heads:
+        raise ValueError(f"q has {H} heads of {D}, the cache {c.kv_heads} of {c.head_dim}")
+    bt, batch, max_pages = _block_table(block_table, dev)
+    lens = _tensor(kv_lens, "kv_lens", dev, torch.int32, (batch,))
+    cu = None if cu_q is None else _tensor(cu_q, "cu_q", dev, torch.int32, (batch + 1,))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
+    ho = _heads(out, "out", dev, q.dtype)
+    lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
+    if workspace is None:
+        workspace = torch.zeros(max(patch_attn_kv8_workspace_size(T, batch, H, cache), 16), dtype=torch.uint8, device=dev)
+    ws = _tensor(workspace, "workspace", dev, torch.uint8)
+    ref = ctypes.byref
+    _call("patch_attn_kv8", dev, stream, ref(hq), T, dt, ref(c), bt, max_pages, lens, cu, batch,
+          1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, ref(ho),
+          None if lse is None else lse.data_ptr(), ws, workspace.numel(), _status(status, dev), tail=(wait_limit_us,))
+    return (out, lse) if want_lse else out
+
+
+# ---- linears with 4-bit weights
+
+
+@dataclass
+class Weight4:
+    """A linear weight in 4 bits: W[n][k] = (code - 8) * scales[n][k // group], codes
+    u8 [N][K // 2] with the even k in the low half of a byte."""
+    codes: torch.Tensor
+    scales: torch.Tensor  # bf16, fp16 or fp32 [N][K // group]
+    group: int
+
+    @property
+    def N(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def K(self) -> int:
+        return 2 * self.codes.shape[1]
+
+    def struct(self) -> _Weight4:
+        if self.group not in GROUPS4:
+            raise ValueError(f"group {self.group}, expected one of {GROUPS4}")
+        if self.codes.dim() != 2 or 2 * self.codes.shape[1] % self.group:
+            raise ValueError(f"codes must be [N][K / 2] with K a multiple of the group ({self.group})")
+        dev = self.codes.device
+        sd = _dtype(self.scales, "scales", tuple(DTYPES))
+        return _Weight4(self.N, self.K, self.group, sd, _tensor(self.codes, "codes", dev, torch.uint8),
+                        _tensor(self.scales, "scales", dev, self.scales.dtype, (self.N, self.K // self.group)))
+
+    @property
+    def stored_bytes(self) -> int:
+        return self.codes.numel() + self.scales.numel() * self.scales.element_size()
+
+
+def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype = torch.bfloat16,
+                    stream=None) -> Weight4:
+    """W (bf16, fp16 or fp32 [N][K]) to 4 bits by rounding under per-group scales amax / 7."""
+    if W.dim() != 2:
+        raise ValueError("W must be [N][K]")
+    N, K = W.shape
+    if group not in GROUPS4 or K % group:
+        raise ValueError(f"group {group}: expected one of {GROUPS4} that divides K = {K}")
+    if scale_dtype not in DTYPES:
+        raise ValueError(f"scale_dtype {scale_dtype}, expected one of {[str(d) for d in DTYPES]}")
+    dev = W.device
+    p = _tensor(W, "W", dev, W.dtype)
+    w4 = Weight4(torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
+                 torch.empty((N, K // group), dtype=scale_dtype, device=dev), group)
+    st = w4.struct()
+    _call("patch_quantize4", dev, stream, p, _dtype(W, "W", tuple(DTYPES)), ctypes.byref(st))
+    return w4
+
+
+def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X * W^T for up to 16 tokens (bf16 or fp16 [M][K]) and a 4-bit weight, fp32 sums."""
+    dev = weight.codes.device
+    st = weight.struct()
+    if X.dim() != 2 or X.shape[1] != st.K:
+        raise ValueError(f"X has shape {tuple(X.shape)}, weight has K={st.K}")
+    M = X.shape[0]
+    dt = _dtype(X, "X")
+    x = _tensor(X, "X", dev, X.dtype)
+    if Y is None:
+        Y = torch.empty((M, st.N), dtype=X.dtype, device=dev)
+    y = _tensor(Y, "Y", dev, X.dtype, (M, st.N))
+    _call("patch_gemm4", dev, stream, x, M, dt, ctypes.byref(st), y)
+    return Y
