@@ -30,7 +30,7 @@ patch_status_t check_cache(const patch_kv8_cache* c) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return PATCH_ERR_INVALID_ARG;
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return PATCH_ERR_SHAPE;
   if (c->head_dim != 64 && c->head_dim != 128) return PATCH_ERR_SHAPE;
-  if (c->n_pages < 1 || c->n_pages > (int64_t(1) << 31) - 1 || c->kv_heads < 1 || c->kv_heads > 65535)
+  if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->n_pages >= (int64_t(1) << 31) / c->kv_heads)
     return PATCH_ERR_SHAPE;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return PATCH_ERR_ALIGN;
   return PATCH_OK;
@@ -171,7 +171,7 @@ static patch_status_t check_attn_sizes(int64_t n_tokens, int64_t batch, int64_t 
   const patch_status_t st = check_cache(cache);
   if (st != PATCH_OK) return st;
   if (q_heads % cache->kv_heads || q_heads / cache->kv_heads > 16 || q_heads > 65535) return PATCH_ERR_SHAPE;
-  if (n_tokens > kMaxCount || batch > kMaxCount / 4) return PATCH_ERR_SHAPE;
+  if (n_tokens > kMaxCount / 16 || batch > kMaxCount / 4) return PATCH_ERR_SHAPE;
   return PATCH_OK;
 }
 
@@ -199,7 +199,7 @@ patch_status_t patch_attn_kv8(const patch_heads* q, int64_t n_tokens, int dtype,
   patch_status_t st = check_attn_sizes(n_tokens, batch, q->heads, cache);
   if (st != PATCH_OK) return st;
   if (out->heads != q->heads || (!cu_q && n_tokens != batch)) return PATCH_ERR_INVALID_ARG;
-  if (max_pages < 0 || max_pages > kMaxCount) return PATCH_ERR_SHAPE;
+  if (max_pages < 0 || max_pages > kMaxCount / cache->page) return PATCH_ERR_SHAPE;
   if (n_tokens == 0 || batch == 0) return PATCH_OK;
   if (!kv_lens || (!block_table && max_pages > 0)) return PATCH_ERR_INVALID_ARG;
   for (const patch_heads* x : {q, out}) {

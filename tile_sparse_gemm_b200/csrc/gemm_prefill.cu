@@ -668,6 +668,20 @@ bool make_map_2d_bf16_sw64(CUtensorMap* map, const void* base, uint64_t inner, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pages of a paged 8-bit cache: 3D map (element, token, page and head) over
+// [n_blocks][page][dim] bytes, boxes of `box` tokens of one block, swizzled by
+// the row's length (dim 64 or 128); a block behind the end reads as zeros.
+bool make_map_pages_u8(CUtensorMap* map, const void* base, int64_t dim, int64_t page, int64_t n_blocks, int box) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(page), cuuint64_t(n_blocks)};
+  const cuuint64_t strides[2] = {cuuint64_t(dim), cuuint64_t(dim * page)};
+  const cuuint32_t boxes[3] = {cuuint32_t(dim), cuuint32_t(box), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Tokens per unit: the multiple of 16 in [64, BT] that minimises the time of
 // the slowest CTA, modelled as (units per CTA, rounded up) x (unit time).  A
