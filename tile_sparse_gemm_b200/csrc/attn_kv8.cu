@@ -11,12 +11,13 @@
 // What bounds it: bytes of the cache (2 D a token and head) for few rows.  So
 // the work is cut by bytes: every (sequence, head, row tile) is a run of chunks
 // of 32 (D = 128) or 64 (D = 64) tokens, 8 KiB of keys and values each, and
-// every CTA (one per SM) takes an equal share of all chunks, wherever tiles
-// begin and end; the sequences' lengths are read on the device.  Each of a
-// CTA's 8 warps fetches its own chunks (every eighth) by TMA into a ring of its
-// own, so no warp waits for another until a tile ends; then the warps' states
-// are joined in a tree.  A tile cut between CTAs is finished by the last of
-// them, which joins the parts in CTA order (deterministic).
+// every warp of every CTA (8 warps, one CTA per SM) takes an equal share of all
+// chunks in a row, wherever tiles begin and end; the sequences' lengths are read
+// on the device.  A warp fetches its chunks by TMA into a ring of its own and
+// waits for no other warp until its share is done.  A tile that lies in one
+// warp's share is written by it; the pieces of the others are joined through
+// shared memory, and of a tile cut between CTAs by the last CTA to arrive, in
+// the order of the pieces (deterministic).
 //
 // Tensor cores (mma.sync m16n8k16, fp16 in, fp32 out): tokens are the 16 rows,
 // queries the 8 columns, S^T = K Q^T and O^T = V^T P^T, since a decode step has
@@ -47,23 +48,25 @@ struct Params {
   uint32_t* counters;  // one per CTA: arrivals at the tile that begins in it and goes on
   float* parts;        // two tile states per CTA
   uint64_t limit_ns;
+  int page_shift, box_shift;  // log2 of a page's and a TMA box's tokens
 };
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int CH = kChunkBytes / D;        // tokens of a chunk
-  static constexpr int SL = CH / 16;                // slices of 16 tokens
-  static constexpr int KS = D / 16;                 // k steps of S, row tiles of O
-  static constexpr int R = 8 * NT;                  // query rows of a tile
+  static constexpr int CH = kChunkBytes / D;  // tokens of a chunk
+  static constexpr int SL = CH / 16;          // slices of 16 tokens
+  static constexpr int KS = D / 16;           // k steps of S, row tiles of O
+  static constexpr int R = 8 * NT;            // query rows of a tile
   static constexpr int STAGES = NT == 1 ? 3 : 2;
-  static constexpr int kStateRegs = 4 * KS * NT + 4 * NT;  // o, m, l of a warp, per lane
-  static constexpr int kStateBytes = kStateRegs * 128;
-  static constexpr int kRing = kWarps * STAGES * 2 * kChunkBytes;
-  static constexpr int kBars = kRing;                                  // full barriers
-  static constexpr int kScales = kBars + kWarps * STAGES * 8;          // ring of scales: 4 slices x (k, v)
-  static constexpr int kSlots = kScales + kWarps * STAGES * 32;        // tree: 7 states
-  static constexpr int kMisc = kSlots + 7 * kStateBytes;
-  static constexpr int kSmem = kMisc + 128 + 1024;                     // and alignment
+  static constexpr int kStateFloats = R * D + 2 * R;  // o, m, l of a tile
+  static constexpr int kStateBytes = kStateFloats * 4;
+  static constexpr int kRingBytes = STAGES * 2 * kChunkBytes;  // of a warp
+  static constexpr int kHeads = kWarps * kRingBytes;           // a state for each warp: the tile it entered in the middle
+  static constexpr int kBars = kHeads + kWarps * kStateBytes;  // full barriers
+  static constexpr int kScales = kBars + kWarps * STAGES * 8;  // ring of scales: up to 4 boxes x (k, v)
+  static constexpr int kPieces = kScales + kWarps * STAGES * 32;
+  static constexpr int kMisc = kPieces + 2 * kWarps * 48;
+  static constexpr int kSmem = kMisc + 256;
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -112,12 +115,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A row tile of one sequence and head: which tokens its rows see.
 struct Tile {
   int b, h, rt;
-  int len, m, row0;     // the sequence's tokens, queries, first row of q
-  int chunk0, chunks;   // its run of chunks (at least one, so that every tile is written)
-  int hi;               // tokens from here on are seen by no row
+  int len, m, row0;    // the sequence's tokens, queries, first row of q
+  int chunk0, chunks;  // its run of chunks (at least one, so that every tile is written)
+  int hi;              // tokens from here on are seen by no row
 };
 
 __device__ __forceinline__ void sequence(const AttnParams& a, int b, int& len, int& m, int& row0) {
@@ -133,10 +140,9 @@ __device__ __forceinline__ void sequence(const AttnParams& a, int b, int& len, i
 
 template <int CH, int R>
 __device__ __forceinline__ void set_rows(const AttnParams& a, int G, Tile& t) {
-  const int i0 = t.rt * R / G, i1 = min(t.m - 1, (t.rt * R + R - 1) / G);
   int hi = t.len, lo = 0;
-  if (a.causal) hi = max(0, min(t.len, t.len - t.m + i1 + 1));
-  if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + i0 - a.window + 1));
+  if (a.causal) hi = max(0, min(t.len, t.len - t.m + min(t.m - 1, (t.rt * R + R - 1) / G) + 1));
+  if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + t.rt * R / G - a.window + 1));
   t.hi = hi;
   t.chunk0 = lo / CH;
   t.chunks = max(1, (hi + CH - 1) / CH - t.chunk0);
@@ -145,140 +151,92 @@ template <int R>
 __device__ __forceinline__ int row_tiles(int m, int G) {
   return (m * G + R - 1) / R;
 }
-// chunks of all of a sequence's tiles of one head
+
+// Shares are equal in units: a chunk is one, and a tile's own cost (its queries,
+// its output; about half a chunk's time in a warp) is kTileUnits in front of its chunks.
+constexpr int kTileUnits = 1;
+
+// units of all of a sequence's tiles of one head
 template <int CH, int R>
-__device__ __forceinline__ int64_t chunks_per_head(const AttnParams& a, int G, int b) {
-  Tile t;
-  sequence(a, b, t.len, t.m, t.row0);
+__device__ __forceinline__ int64_t units_per_head(const AttnParams& a, int G, Tile& t) {
   const int n = row_tiles<R>(t.m, G);
   if (n == 0) return 0;
   if (!a.causal) {
     t.rt = 0;
     set_rows<CH, R>(a, G, t);
-    return int64_t(n) * t.chunks;
+    return int64_t(n) * (t.chunks + kTileUnits);
   }
   int64_t s = 0;
   for (t.rt = 0; t.rt < n; ++t.rt) {
     set_rows<CH, R>(a, G, t);
-    s += t.chunks;
+    s += t.chunks + kTileUnits;
   }
   return s;
 }
-// to the next tile, in the order (sequence, head, row tile); past the last one b == batch
+// to the next tile, in the order (sequence, head, row tile)
 template <int CH, int R>
 __device__ __forceinline__ void next_tile(const AttnParams& a, int G, Tile& t) {
-  if (++t.rt < row_tiles<R>(t.m, G)) {
-    set_rows<CH, R>(a, G, t);
-    return;
-  }
-  t.rt = 0;
-  if (++t.h == a.kv_heads) {
-    t.h = 0;
-    do {
-      if (++t.b >= a.batch) return;
-      sequence(a, t.b, t.len, t.m, t.row0);
-    } while (t.m == 0);
+  if (++t.rt >= row_tiles<R>(t.m, G)) {
+    t.rt = 0;
+    if (++t.h == a.kv_heads) {
+      t.h = 0;
+      do {
+        if (++t.b >= a.batch) return;
+        sequence(a, t.b, t.len, t.m, t.row0);
+      } while (t.m == 0);
+    }
   }
   set_rows<CH, R>(a, G, t);
 }
 
-// A warp's softmax state of a tile, in the layout of the O^T accumulators:
-// lane (n = lane / 4, q = lane % 4) holds rows 8 nt + 2q + e of the tile and,
-// of D = 128, elements 16 n + 2 j + {0, 1} (8 n + 2 j + {0, 1} of D = 64) in
-// o[j][nt][2 * which + e].
-template <int D, int NT>
-struct State {
-  float o[D / 16][NT][4];
-  float m[NT][2], l[NT][2];
+// A warp's place in its share: chunks c .. c_end - 1 of tile t are next, `left`
+// units of the share count from the tile's first on.  c == c_end: done.
+struct Cursor {
+  Tile t;
+  int c, c_end;
+  int64_t left;
 
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nt][e] = -INFINITY;
-        l[nt][e] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][nt][i] = 0.0f;
-    }
-  }
-  // p: 32-lane columns of floats, this lane's column
-  __device__ __forceinline__ void store(float* p) const {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[(4 * nt + e) * 32] = m[nt][e];
-        p[(4 * nt + 2 + e) * 32] = l[nt][e];
-      }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[(4 * NT + (j * NT + nt) * 4 + i) * 32] = o[j][nt][i];
-    }
-  }
-  // join with a stored state; kGlobal: written by another CTA (read past L1)
-  template <bool kGlobal>
-  __device__ __forceinline__ void join(const float* p) {
-    auto get = [&](int i) { return kGlobal ? __ldcg(p + i * 32) : p[i * 32]; };
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float fa[2], fb[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mb = get(4 * nt + e), lb = get(4 * nt + 2 + e);
-        const float mx = fmaxf(m[nt][e], mb), base = mx == -INFINITY ? 0.0f : mx;
-        fa[e] = ex2(m[nt][e] - base);
-        fb[e] = ex2(mb - base);
-        m[nt][e] = mx;
-        l[nt][e] = l[nt][e] * fa[e] + lb * fb[e];
-      }
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[j][nt][i] = o[j][nt][i] * fa[i & 1] + get(4 * NT + (j * NT + nt) * 4 + i) * fb[i & 1];
-    }
+  __device__ __forceinline__ void clip() { c_end = int(min(int64_t(t.chunks), max(left - kTileUnits, int64_t(0)))); }
+  template <int CH, int R>
+  __device__ __forceinline__ void next(const AttnParams& a, int G) {
+    left -= t.chunks + kTileUnits;
+    c = c_end = 0;
+    if (left <= kTileUnits) return;
+    next_tile<CH, R>(a, G, t);
+    clip();
   }
 };
 
-// Join the 8 warps' states into warp 0's.  Three rounds over slots of their
-// own (0-3, 4-5, 6): a slot is written again only behind a barrier that its
-// reader has passed.
-template <int D, int NT>
-__device__ __forceinline__ void tree(State<D, NT>& s, uint8_t* slots, int warp, int lane) {
-  constexpr int kBytes = Cfg<D, NT>::kStateBytes;
-  auto slot = [&](int i) { return reinterpret_cast<float*>(slots + i * kBytes) + lane; };
-  if (warp >= 4) s.store(slot(warp - 4));
-  __syncthreads();
-  if (warp < 4) s.template join<false>(slot(warp));
-  if (warp == 2 || warp == 3) s.store(slot(warp + 2));
-  __syncthreads();
-  if (warp < 2) s.template join<false>(slot(warp + 4));
-  if (warp == 1) s.store(slot(6));
-  __syncthreads();
-  if (warp == 0) s.template join<false>(slot(6));
+// A piece of a tile that one warp did not do alone.
+struct Piece {
+  int valid, ends;  // ends: it holds the tile's last chunk
+  int row0, m, rt, h, chunks, pad;
+  int64_t unit0;    // of the tile
+  int64_t pad2;
+};
+static_assert(sizeof(Piece) == 48, "kPieces");
+
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
 }
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_constant__ Params P) {
   using C = Cfg<D, NT>;
   constexpr int CH = C::CH, SL = C::SL, KS = C::KS, R = C::R, STAGES = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const AttnParams& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q4 = lane & 3;
   const int G = a.heads / a.kv_heads;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars) + warp * STAGES;
   float* scales = reinterpret_cast<float*>(smem + C::kScales) + warp * STAGES * 8;
-  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // 8 words of scan, abort flag
-  int* abort_flag = reinterpret_cast<int*>(misc + 12);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // 8 sums, 8 x (sequence, units before it)
+  int* abort_flag = reinterpret_cast<int*>(misc + 24);
   if (lane == 0) {
     for (int s = 0; s < STAGES; ++s) tc::mbar_init(bars + s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pieces[2 * warp].valid = pieces[2 * warp + 1].valid = 0;
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -287,13 +245,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // queries, lengths and cache come from earlier kernels
 
-  // This CTA's share of all chunks: [u0, u1) of W.
-  int64_t part = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    part += chunks_per_head<CH, R>(a, G, b);
-    const int len = a.kv_lens[b];
-    if (blockIdx.x == 0 && (len < 0 || len > a.max_pages * a.page)) set_status(a.status, PATCH_DEV_BOUNDS);
-  }
+  // ---- this CTA's share of all units, [u0, u1) of W, and each warp's first sequence
+  auto units_of = [&](int b) -> int64_t {
+    if (b >= a.batch) return 0;
+    Tile t;
+    sequence(a, b, t.len, t.m, t.row0);
+    return units_per_head<CH, R>(a, G, t) * a.kv_heads;
+  };
   auto warp_scan = [&](int64_t v) {  // inclusive
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -302,108 +260,126 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     }
     return v;
   };
-  const int64_t sum = warp_scan(part);
-  if (lane == 31) misc[warp] = sum;
-  __syncthreads();
-  int64_t W = 0;
+  const int64_t mine = units_of(threadIdx.x);  // the only sequences unless there are more than threads
+  int64_t rest = 0;
+  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) rest += units_of(b);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+      const int len = a.kv_lens[b];
+      if (len < 0 || len > a.max_pages * a.page) set_status(a.status, PATCH_DEV_BOUNDS);
+    }
+  int64_t in = warp_scan(mine), W = 0;
+  {
+    const int64_t all = a.batch > kThreads ? warp_scan(mine + rest) : in;
+    if (lane == 31) misc[warp] = all;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) W += misc[w];
-  W *= a.kv_heads;
+    for (int w = 0; w < kWarps; ++w) W += misc[w];
+  }
   const int64_t n_cta = min(int64_t(gridDim.x), W);
   if (blockIdx.x >= n_cta) return;
-  const int64_t u0 = W * blockIdx.x / n_cta, u1 = W * (blockIdx.x + 1) / n_cta;
-  // the sequence that chunk u0 lies in, and the chunks before it
+  // the first `more` CTAs take per + 1 units, the others per
+  const int64_t per = quotient(W, n_cta), more = W - per * n_cta;
+  const int64_t u0 = per * blockIdx.x + min(int64_t(blockIdx.x), more), u_n = per + (blockIdx.x < more ? 1 : 0);
+  auto owner = [&](int64_t u) {  // the CTA that a unit belongs to
+    const int64_t cut = more * (per + 1);
+    return u < cut ? quotient(u, per + 1) : more + quotient(u - cut, per);
+  };
   int64_t before = 0;
   for (int base = 0; base < a.batch; base += kThreads) {
-    const int b = base + threadIdx.x;
-    const int64_t v = b < a.batch ? chunks_per_head<CH, R>(a, G, b) * a.kv_heads : 0;
-    const int64_t in = warp_scan(v);
-    __syncthreads();
-    if (lane == 31) misc[warp] = in;
-    __syncthreads();
+    const int64_t v = base ? units_of(base + threadIdx.x) : mine;
+    if (base || a.batch > kThreads) {
+      if (base) in = warp_scan(v);
+      __syncthreads();
+      if (lane == 31) misc[warp] = in;
+      __syncthreads();
+    }
     int64_t ex = before + in - v;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) ex += misc[w];
       before += misc[w];
     }
-    if (ex <= u0 && u0 < ex + v) {
-      misc[8] = b;
-      misc[9] = ex;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int64_t u = u0 + (u_n * w >> 3);
+      if (ex <= u && u < ex + v) {
+        misc[8 + 2 * w] = base + threadIdx.x;
+        misc[9 + 2 * w] = ex;
+      }
     }
-    if (before > u0) break;
+    if (before >= u0 + u_n) break;
   }
   __syncthreads();
-  Tile t;
-  t.b = int(misc[8]);
-  int64_t c_seg;  // the first chunk of this CTA's part of tile t
+
+  // ---- this warp's share
+  Cursor cur;
   {
+    const int64_t v0 = u0 + (u_n * warp >> 3), v1 = u0 + (u_n * (warp + 1) >> 3);
+    Tile& t = cur.t;
+    t.b = int(misc[8 + 2 * warp]);
     sequence(a, t.b, t.len, t.m, t.row0);
-    const int64_t off = u0 - misc[9], per_head = chunks_per_head<CH, R>(a, G, t.b);
-    t.h = int(off / per_head);
-    c_seg = off % per_head;
+    int64_t off = v0 - misc[9 + 2 * warp];
+    const int64_t per_head = units_per_head<CH, R>(a, G, t);
+    t.h = int(quotient(off, per_head));
+    off -= per_head * t.h;
     t.rt = 0;
     set_rows<CH, R>(a, G, t);
-    while (c_seg >= t.chunks) {
-      c_seg -= t.chunks;
+    while (off >= t.chunks + kTileUnits) {
+      off -= t.chunks + kTileUnits;
       ++t.rt;
       set_rows<CH, R>(a, G, t);
     }
+    cur.left = v1 - (v0 - off);
+    cur.c = int(max(off - kTileUnits, int64_t(0)));
+    cur.clip();
   }
 
-  // This warp's chunks are u0 + warp, u0 + warp + 8, ...: a cursor runs ahead of the work and fetches.
-  const uint32_t ring = tc::smem_u32(smem) + warp * STAGES * 2 * kChunkBytes;
-  const int box = min(a.page, CH), boxes = CH / box;
-  Tile ft = t;
-  int64_t fc = c_seg + warp, fu = u0 + warp;
+  // ---- a second cursor runs ahead and fetches
+  const uint32_t ring = tc::smem_u32(smem) + warp * C::kRingBytes;
+  Cursor fet = cur;
   int issued = 0;
   auto fetch = [&]() {  // the whole warp
-    if (fu >= u1) return;
-    while (fc >= ft.chunks) {
-      fc -= ft.chunks;
-      next_tile<CH, R>(a, G, ft);
-    }
-    const int st = issued % STAGES;
-    const int t0 = (ft.chunk0 + int(fc)) * CH;
-    const int n_box = min(boxes, (ft.hi - t0 + box - 1) / box);  // none in a tile that sees nothing
-    const uint32_t bar = tc::smem_u32(bars + st);
-    if (lane == 0) {
-      if (n_box > 0)
-        tc::mbar_expect_tx(bars + st, uint32_t(n_box * box * D * 2));
-      else
-        tc::mbar_arrive(bars + st);
-    }
-    __syncwarp();
-    if (lane < n_box) {
-      const int tok = t0 + lane * box;
-      const int64_t phys = a.block_table[ft.b * a.max_pages + tok / a.page];
-      const bool ok = phys >= 0 && phys < a.n_pages;
-      if (!ok) set_status(a.status, PATCH_DEV_BOUNDS);
-      const int64_t blk = ok ? phys * a.kv_heads + ft.h : a.n_pages * a.kv_heads;  // behind the end: reads zeros
-      const uint32_t dst = ring + st * 2 * kChunkBytes + lane * box * D;
-      tma_load_3d(dst, &P.k_map, bar, 0, tok % a.page, int(blk));
-      tma_load_3d(dst + kChunkBytes, &P.v_map, bar, 0, tok % a.page, int(blk));
-      const float ks = ok ? a.k_scale[blk] : 1.0f, vs = ok ? a.v_scale[blk] : 1.0f;
-      for (int i = 0; i < box / 16; ++i) {
-        scales[st * 8 + 2 * (lane * (box / 16) + i)] = ks;
-        scales[st * 8 + 2 * (lane * (box / 16) + i) + 1] = vs;
+    if (fet.c < fet.c_end) {
+      const int st = issued % STAGES;
+      const int t0 = (fet.t.chunk0 + fet.c) * CH;
+      const int box = 1 << P.box_shift;
+      const int n_box = min(CH >> P.box_shift, (fet.t.hi - t0 + box - 1) >> P.box_shift);  // < 1: a tile that sees nothing
+      const uint32_t bar = tc::smem_u32(bars + st);
+      if (lane == 0) {
+        if (n_box > 0)
+          tc::mbar_expect_tx(bars + st, uint32_t(n_box) * uint32_t(2 * D) << P.box_shift);
+        else
+          tc::mbar_arrive(bars + st);
       }
+      __syncwarp();
+      if (lane < n_box) {
+        const int tok = t0 + (lane << P.box_shift), in_page = tok & (a.page - 1);
+        const int phys = a.block_table[fet.t.b * a.max_pages + (tok >> P.page_shift)];
+        const bool ok = phys >= 0 && phys < a.n_pages;
+        if (!ok) set_status(a.status, PATCH_DEV_BOUNDS);
+        const int blk = ok ? phys * a.kv_heads + fet.t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
+        const uint32_t dst = ring + st * 2 * kChunkBytes + lane * (D << P.box_shift);
+        tma_load_3d(dst, &P.k_map, bar, 0, in_page, blk);
+        tma_load_3d(dst + kChunkBytes, &P.v_map, bar, 0, in_page, blk);
+        // a box's scales, asynchronously too (a page outside the pool reads as zeros under any scale)
+        const int sc = ok ? blk : 0;
+        cp_async4(scales + st * 8 + 2 * lane, a.k_scale + sc);
+        cp_async4(scales + st * 8 + 2 * lane + 1, a.v_scale + sc);
+      }
+      ++issued;
+      if (++fet.c == fet.c_end) fet.next<CH, R>(a, G);
     }
-    __syncwarp();  // the scales are for the whole warp
-    ++issued;
-    fu += kWarps;
-    fc += kWarps;
+    asm volatile("cp.async.commit_group;" ::: "memory");  // one group a call, on every lane
   };
   for (int s = 0; s < STAGES; ++s) fetch();
 
   int done = 0;
-  State<D, NT> S;
-  for (int64_t u = u0; u < u1;) {
-    // ---- this CTA's chunks c_seg .. c_end - 1 of tile t
-    const int64_t tile_u0 = u - c_seg;
-    const int64_t c_end = min(int64_t(t.chunks), c_seg + (u1 - u));
-    // the rows' queries as operands, each row divided by a power of two
+  for (; cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
+    const Tile& t = cur.t;
+    // ---- the rows' queries as operands, each row divided by a power of two
     uint32_t qf[NT][KS][2];
-    float row_scale[NT][2];   // of this lane's accumulator columns 2 q4, 2 q4 + 1
+    float row_scale[NT][2];  // of this lane's accumulator columns 2 q4, 2 q4 + 1
     int see_lo[NT][2], see_hi[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -447,16 +423,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     const int all_hi = a.causal ? t.len - t.m + t.rt * R / G + 1 : t.len;  // every row sees the tokens before it ...
     const int last_row = min(t.m - 1, (t.rt * R + R - 1) / G);
     const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;  // ... from here on
-    S.clear();
-    float v_ref = 0.0f;
 
-    for (int64_t c = c_seg + (((u0 + warp - u) % kWarps) + kWarps) % kWarps; c < c_end; c += kWarps) {
+    // The softmax state in the layout of the O^T accumulators: rows 8 nt + 2 q4 + e
+    // of the tile; elements 16 n + 2 j + {0, 1} (D = 64: 8 n + 2 j + {0, 1}) in o[j][nt][2 {0, 1} + e].
+    float o[KS][NT][4], m[NT][2], l[NT][2], v_ref = 0.0f, v_inv = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][nt][i] = 0.0f;
+    }
+
+    for (int c = cur.c; c < cur.c_end; ++c) {
       const int st = done % STAGES;
       const bool ok = tc::wait_bounded(bars + st, (done / STAGES) & 1, abort_flag, P.limit_ns, a.status, false);
       ++done;
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");  // this stage's scales
+      __syncwarp();
       const uint32_t ks_at = ring + st * 2 * kChunkBytes, vs_at = ks_at + kChunkBytes;
-      const int t0 = (t.chunk0 + int(c)) * CH;
+      const int t0 = (t.chunk0 + c) * CH;
       // ---- scores
       float s[SL][NT][4];
 #pragma unroll
@@ -491,27 +480,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
         }
       }
       // ---- softmax
-      float v_new = v_ref;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = S.m[nt][0], mx[nt][1] = S.m[nt][1];
       const bool some_hidden = t0 + CH > all_hi || t0 < all_lo;
+      float mx[NT][2], v_new = v_ref, vs[SL];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mx[nt][0] = m[nt][0], mx[nt][1] = m[nt][1];
 #pragma unroll
       for (int sl = 0; sl < SL; ++sl) {
-        const float ks = scales[st * 8 + 2 * sl];
-        // a slice that no row sees may not have been fetched: its scale is left out
-        if (t0 + 16 * sl < t.hi) v_new = fmaxf(v_new, scales[st * 8 + 2 * sl + 1]);
+        const float2 sc = *reinterpret_cast<const float2*>(scales + st * 8 + 2 * ((16 * sl) >> P.box_shift));
+        vs[sl] = sc.y;
+        if (some_hidden && t0 + 16 * sl >= t.hi) vs[sl] = 0.0f;  // seen by no row and perhaps not fetched
+        v_new = fmaxf(v_new, vs[sl]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = i & 1, tok = t0 + 16 * sl + n + 8 * (i >> 1);
-            float x = s[sl][nt][i] * (ks * row_scale[nt][e]);
-            if (some_hidden && (tok >= see_hi[nt][e] || tok < see_lo[nt][e])) x = -INFINITY;
-            s[sl][nt][i] = x;
-            mx[nt][e] = fmaxf(mx[nt][e], x);
-          }
+          for (int i = 0; i < 4; ++i) s[sl][nt][i] *= sc.x * row_scale[nt][i & 1];
       }
+      if (some_hidden) {
+#pragma unroll
+        for (int sl = 0; sl < SL; ++sl)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = t0 + 16 * sl + n + 8 * (i >> 1);
+              if (tok >= see_hi[nt][i & 1] || tok < see_lo[nt][i & 1]) s[sl][nt][i] = -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int sl = 0; sl < SL; ++sl)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[nt][i & 1] = fmaxf(mx[nt][i & 1], s[sl][nt][i]);
       bool grew = v_new != v_ref;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -519,48 +519,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xFFFFFFFFu, mx[nt][e], d));
-          grew |= mx[nt][e] != S.m[nt][e];
+          grew |= mx[nt][e] != m[nt][e];
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
-        const float fv = v_new > 0.0f ? __fdiv_rn(v_ref, v_new) : 0.0f;
+        if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
+        const float fv = v_ref * v_inv;  // of the values summed so far
+        v_ref = v_new;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = mx[nt][e] == -INFINITY ? 1.0f : ex2(S.m[nt][e] - mx[nt][e]);
-            S.m[nt][e] = mx[nt][e];
-            S.l[nt][e] *= f;
+            const float f = mx[nt][e] == -INFINITY ? 1.0f : ex2(m[nt][e] - mx[nt][e]);
+            m[nt][e] = mx[nt][e];
+            l[nt][e] *= f;
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
-              S.o[j][nt][e] *= f * fv;
-              S.o[j][nt][2 + e] *= f * fv;
+              o[j][nt][e] *= f * fv;
+              o[j][nt][2 + e] *= f * fv;
             }
           }
-        v_ref = v_new;
       }
       uint32_t pb[SL][NT][2];
 #pragma unroll
-      for (int sl = 0; sl < SL; ++sl) {
-        const float vr = t0 + 16 * sl < t.hi && v_ref > 0.0f ? __fdiv_rn(scales[st * 8 + 2 * sl + 1], v_ref) : 0.0f;
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float m = S.m[nt][i & 1];
-            p[i] = ex2(s[sl][nt][i] - (m == -INFINITY ? 0.0f : m));
-            S.l[nt][i & 1] += p[i];
-          }
+        for (int sl = 0; sl < SL; ++sl) {
+          const float vr = vs[sl] * v_inv;
+          const float p0 = ex2(s[sl][nt][0] - m0), p1 = ex2(s[sl][nt][1] - m1);
+          const float p2 = ex2(s[sl][nt][2] - m0), p3 = ex2(s[sl][nt][3] - m1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
           // fp16 probabilities: 11 bits against the 4 of the values they weigh
-          pb[sl][nt][0] = transpose8x8(pack_f16(p[0] * vr, p[1] * vr));
-          pb[sl][nt][1] = transpose8x8(pack_f16(p[2] * vr, p[3] * vr));
+          pb[sl][nt][0] = transpose8x8(pack_f16(p0 * vr, p1 * vr));
+          pb[sl][nt][1] = transpose8x8(pack_f16(p2 * vr, p3 * vr));
         }
       }
       // ---- values
 #pragma unroll
       for (int sl = 0; sl < SL; ++sl) {
-        constexpr int NW = D / 32;   // words of a lane's piece of a row
-        uint32_t w[4][NW];           // tokens 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9 of the slice
+        constexpr int NW = D / 32;  // words of a lane's piece of a row
+        uint32_t w[4][NW];          // tokens 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9 of the slice
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int r = 16 * sl + 2 * q4 + (k & 1) + 8 * (k >> 1);
@@ -571,18 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
             const uint2 x = lds64(vs_at + r * 64 + uint32_t((n >> 1) ^ ((r >> 1) & 3)) * 16 + (n & 1) * 8);
             w[k][0] = x.x, w[k][1] = x.y;
           }
-          if (some_hidden && t0 + r >= t.hi)  // behind the tokens: anything may lie there
-#pragma unroll
-            for (int i = 0; i < NW; ++i) w[k][i] = 0;
         }
         if (some_hidden) {
-          // A NaN value must not reach a row that does not see its token (0 x NaN): take
-          // it out here and put it back where it is seen, by counting with the tensor cores.
           bool bad = false;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) {
+            const bool behind = t0 + 16 * sl + 2 * q4 + (k & 1) + 8 * (k >> 1) >= t.hi;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) bad |= __vcmpeq4(w[k][i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+            for (int i = 0; i < NW; ++i) {
+              if (behind) w[k][i] = 0;  // behind the tokens anything may lie
+              bad |= __vcmpeq4(w[k][i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+            }
+          }
+          // A NaN value must not reach a row that does not see its token (0 x NaN): take
+          // it out here and put it back where it is seen, by counting with the tensor cores.
           if (__any_sync(0xFFFFFFFFu, bad)) {
             uint32_t seen[NT][2];
 #pragma unroll
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
                   mma_f16(cnt, a0, a1, a2, a3, seen[nt][0], seen[nt][1]);
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
-                    if (cnt[k] > 0.0f) S.o[2 * i + p][nt][k] = __int_as_float(0x7FC00000);
+                    if (cnt[k] > 0.0f) o[2 * i + p][nt][k] = __int_as_float(0x7FC00000);
                 }
               }
             }
@@ -627,54 +628,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
             cvt4(__byte_perm(w[0][i], w[1][i], p ? 0x7362 : 0x5140), a0, a1);
             cvt4(__byte_perm(w[2][i], w[3][i], p ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(S.o[2 * i + p][nt], a0, a1, a2, a3, pb[sl][nt][0], pb[sl][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * i + p][nt], a0, a1, a2, a3, pb[sl][nt][0], pb[sl][nt][1]);
           }
       }
       __syncwarp();  // every lane has read the stage
       fetch();
     }
 
-    // ---- the tile's state over this CTA's chunks, in warp 0
+    // ---- the tile's state over this warp's chunks: out, or kept as a piece
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) S.l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, S.l[nt][e], d);
+        for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], d);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          S.o[j][nt][e] *= v_ref;
-          S.o[j][nt][2 + e] *= v_ref;
+          o[j][nt][e] *= v_ref;
+          o[j][nt][2 + e] *= v_ref;
         }
       }
-    tree<D, NT>(S, smem + C::kSlots, warp, lane);
-    bool write = warp == 0;
-    if (c_seg > 0 || c_end < t.chunks) {  // a cut tile
-      const int64_t first = ((tile_u0 + 1) * n_cta - 1) / W, last = ((tile_u0 + t.chunks) * n_cta - 1) / W;
-      constexpr int64_t kState = C::kStateRegs * 32;
-      int* flag = abort_flag + 1;
-      if (warp == 0) {
-        S.store(P.parts + (2 * blockIdx.x + (blockIdx.x == first ? 1 : 0)) * kState + lane);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) *flag = atomicAdd(P.counters + first, 1u) == uint32_t(last - first);
-      }
-      __syncthreads();
-      const bool is_last = *flag != 0;
-      write = false;
-      if (is_last) {  // the last to arrive joins the parts, in CTA order
-        __threadfence();
-        S.clear();
-        for (int64_t i = first + warp; i <= last; i += kWarps)
-          S.template join<true>(P.parts + (2 * i + (i == first ? 1 : 0)) * kState + lane);
-        tree<D, NT>(S, smem + C::kSlots, warp, lane);
-        write = warp == 0;
-        if (threadIdx.x == 0) P.counters[first] = 0;
-      }
-      __syncthreads();  // the flag is read before the next cut tile writes it
-    }
-    if (write) {
-      constexpr int kStep = D / 8;  // elements of a lane
+    const bool begins = cur.c == 0, ends = cur.c_end == t.chunks;
+    constexpr int kStep = D / 8;  // elements of a lane in a row
+    if (begins && ends) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -683,28 +659,139 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
           if (r >= t.m * G) continue;
           const int64_t row = t.row0 + r / G;
           const int head = t.h * G + r % G;
-          const float inv = S.m[nt][e] == -INFINITY && S.l[nt][e] == 0.0f ? 0.0f : 1.0f / S.l[nt][e];
+          const bool none = m[nt][e] == -INFINITY && l[nt][e] == 0.0f;
+          const float inv = none ? 0.0f : 1.0f / l[nt][e];
           T* dst = static_cast<T*>(a.out) + row * a.o_ts + head * a.o_hs + kStep * n;
           float x[kStep];
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
-            x[2 * j] = S.o[j][nt][e] * inv;
-            x[2 * j + 1] = S.o[j][nt][2 + e] * inv;
+            x[2 * j] = o[j][nt][e] * inv;
+            x[2 * j + 1] = o[j][nt][2 + e] * inv;
           }
 #pragma unroll
           for (int j = 0; j < kStep / 8; ++j) store16(dst + 8 * j, x + 8 * j);
-          if (a.lse && n == 0)
-            a.lse[row * a.heads + head] =
-                S.m[nt][e] == -INFINITY && S.l[nt][e] == 0.0f ? -INFINITY : (S.m[nt][e] + log2f(S.l[nt][e])) / kLog2e;
+          if (a.lse && n == 0) a.lse[row * a.heads + head] = none ? -INFINITY : (m[nt][e] + log2f(l[nt][e])) / kLog2e;
         }
+    } else {
+      // Entered in the middle: its own place, work goes on.  Left in the middle: the share is
+      // done, and the state takes the place of the ring.
+      float* keep = reinterpret_cast<float*>(begins ? smem + warp * C::kRingBytes : smem + C::kHeads + warp * C::kStateBytes);
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (n == 0) {
+            keep[R * D + 8 * nt + 2 * q4 + e] = m[nt][e];
+            keep[R * D + R + 8 * nt + 2 * q4 + e] = l[nt][e];
+          }
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) keep[((j * NT + nt) * 4 + 2 * x + e) * 32 + lane] = o[j][nt][2 * x + e];
+        }
+      if (lane == 0) pieces[2 * warp + begins] = Piece{1, ends, t.row0, t.m, t.rt, t.h, t.chunks, 0, u0 + (u_n * (warp + 1) >> 3) - cur.left, 0};
     }
-    u += c_end - c_seg;
-    c_seg = 0;
-    next_tile<CH, R>(a, G, t);
   }
-  // after a timeout: let the copies in flight land before the shared memory goes
+  // after a timeout: let the copies in flight land before their memory is used again
   for (; done < issued; ++done)
     tc::wait_bounded(bars + done % STAGES, (done / STAGES) & 1, abort_flag, P.limit_ns, a.status, true);
+
+  // ---- join the pieces: a run of one tile's pieces is the one that begins it (or comes in from the
+  // CTA before) and the following warps' that entered it in the middle.  Every thread joins kEl
+  // elements in a row of one of the tile's rows.
+  __syncthreads();
+  constexpr int kPerRow = kThreads / R, kEl = D / kPerRow;
+  const int row = threadIdx.x / kPerRow, d0 = (threadIdx.x % kPerRow) * kEl;
+  auto piece_at = [&](int i) {
+    return reinterpret_cast<const float*>((i & 1) ? smem + (i >> 1) * C::kRingBytes : smem + C::kHeads + (i >> 1) * C::kStateBytes);
+  };
+  auto element = [&](int i) {  // place of element d0 + i of the row in a piece
+    constexpr int kStep = D / 8;
+    const int d = d0 + i, j = (d % kStep) >> 1;
+    return ((j * NT + (row >> 3)) * 4 + 2 * (d & 1) + (row & 1)) * 32 + 4 * (d / kStep) + ((row & 7) >> 1);
+  };
+  for (int i = 0; i < 2 * kWarps;) {
+    if (!pieces[i].valid) {
+      ++i;
+      continue;
+    }
+    const Piece first = pieces[i];
+    float x[kEl], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEl; ++k) x[k] = 0.0f;
+    const bool comes_in = (i & 1) == 0;
+    bool ends = false;
+    do {
+      if (pieces[i].valid) {
+        const float* p = piece_at(i);
+        const float mp = p[R * D + row], lp = p[R * D + R + row];
+        const float mn = fmaxf(m, mp), base = mn == -INFINITY ? 0.0f : mn;
+        const float fa = ex2(m - base), fb = ex2(mp - base);
+        m = mn;
+        l = l * fa + lp * fb;
+#pragma unroll
+        for (int k = 0; k < kEl; ++k) x[k] = x[k] * fa + p[element(k)] * fb;
+        ends = pieces[i].ends;
+      }
+      ++i;
+    } while (!ends && i < 2 * kWarps && !(pieces[i].valid && (i & 1)));
+    bool write = true;
+    if (comes_in || !ends) {  // cut between CTAs
+      const int64_t c0 = owner(first.unit0 + kTileUnits), c1 = owner(first.unit0 + kTileUnits + first.chunks - 1);
+      float* part = P.parts + (2 * blockIdx.x + (comes_in ? 0 : 1)) * int64_t(C::kStateFloats);
+#pragma unroll
+      for (int k = 0; k < kEl; ++k) part[row * D + d0 + k] = x[k];
+      if (d0 == 0) {
+        part[R * D + row] = m;
+        part[R * D + R + row] = l;
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const bool last = atomicAdd(P.counters + c0, 1u) == uint32_t(c1 - c0);
+        if (last) P.counters[c0] = 0;
+        abort_flag[1] = last;
+      }
+      __syncthreads();
+      write = abort_flag[1] != 0;
+      if (write) {  // the last to arrive joins the parts, in CTA order
+        __threadfence();
+        const float* parts = P.parts + (2 * c0 + 1) * int64_t(C::kStateFloats);  // then 2 (c0 + 1), 2 (c0 + 2), ...
+        auto part_of = [&](int64_t c) { return c == c0 ? parts : P.parts + 2 * c * int64_t(C::kStateFloats); };
+        m = -INFINITY;
+#pragma unroll 8
+        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part_of(c) + R * D + row));
+        const float base = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kEl; ++k) x[k] = 0.0f;
+#pragma unroll 4
+        for (int64_t c = c0; c <= c1; ++c) {
+          const float* p = part_of(c);
+          const float f = ex2(__ldcg(p + R * D + row) - base);
+          l += __ldcg(p + R * D + R + row) * f;
+#pragma unroll
+          for (int k = 0; k < kEl; k += 2) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * D + d0 + k));
+            x[k] += y.x * f;
+            x[k + 1] += y.y * f;
+          }
+        }
+      }
+    }
+    const int r = first.rt * R + row;
+    if (write && r < first.m * G) {
+      const int64_t at = first.row0 + r / G;
+      const int head = first.h * G + r % G;
+      const bool none = m == -INFINITY && l == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / l;
+      T* dst = static_cast<T*>(a.out) + at * a.o_ts + head * a.o_hs + d0;
+#pragma unroll
+      for (int k = 0; k < kEl; ++k) dst[k] = from_f32<T>(x[k] * inv);
+      if (a.lse && d0 == 0) a.lse[at * a.heads + head] = none ? -INFINITY : (m + log2f(l)) / kLog2e;
+    }
+  }
 }
 
 template <typename T, int D, int NT>
@@ -735,6 +822,8 @@ cudaError_t launch_attn_kv8(const AttnParams& a, int head_dim, int dtype, void* 
   P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_counter_bytes(num_sms));
   P.limit_ns = limit_ns;
   const int ch = attn::kChunkBytes / head_dim, box = a.page < ch ? a.page : ch;
+  for (P.page_shift = 4; (1 << P.page_shift) < a.page;) ++P.page_shift;
+  for (P.box_shift = 4; (1 << P.box_shift) < box;) ++P.box_shift;
   if (!make_map_pages_u8(&P.k_map, a.k, head_dim, a.page, a.n_pages * a.kv_heads, box) ||
       !make_map_pages_u8(&P.v_map, a.v, head_dim, a.page, a.n_pages * a.kv_heads, box))
     return cudaErrorInvalidValue;
