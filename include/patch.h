@@ -888,10 +888,11 @@ PATCH_API patch_status_t patch_quantize4(const void *W, int dtype, const patch_w
  * weight: the decode product of a linear the tile mask leaves alone (a
  * vocabulary head, small projections).  X [M][K] and Y [M][N] bf16 or fp16
  * (16-byte aligned X), fp32 sums, one rounding.  No workspace; deterministic.
- * Launched with programmatic dependent launch: it reads W before the previous
- * kernel in the stream has completed, X only after.
+ * X enters the tensor cores as fp16, every 128 elements of a token divided by a
+ * power of two first (elements below 2^-28 of the largest lose bits, less than
+ * 2^-39 of it); a token with an infinity or NaN in it gives NaN.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, M outside 0 .. 16, group, dtypes),
- * PATCH_ERR_SHAPE (N < 1, K not a positive multiple of group, either > 2^31 - 1),
+ * PATCH_ERR_SHAPE (N < 1, K not a positive multiple of group, either > 2^30),
  * PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.  M == 0 is a no-op.
  */
 PATCH_API patch_status_t patch_gemm4(const void *X, int64_t M, int dtype, const patch_weight4 *W, void *Y,

@@ -251,7 +251,7 @@ static patch_status_t check_weight4(const patch_weight4* W) {
   if (!W || !W->codes || !W->scales) return PATCH_ERR_INVALID_ARG;
   if (W->group != 32 && W->group != 64 && W->group != 128) return PATCH_ERR_INVALID_ARG;
   if (W->scale_dtype != PATCH_DTYPE_FP32 && !half_type(W->scale_dtype)) return PATCH_ERR_INVALID_ARG;
-  if (W->N < 1 || W->K < 1 || W->K % W->group || W->N >= (int64_t(1) << 31) || W->K >= (int64_t(1) << 31))
+  if (W->N < 1 || W->K < 1 || W->K % W->group || W->N > kMaxCount || W->K > kMaxCount)
     return PATCH_ERR_SHAPE;
   if (!aligned16(W->codes) || !aligned16(W->scales)) return PATCH_ERR_ALIGN;
   return PATCH_OK;

@@ -11,7 +11,6 @@ the kernels report (patch_read_status).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -64,47 +63,69 @@ def signatures() -> dict:
     }
 
 
+_byref = ctypes.byref
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from CPU-only builds of torch
+
+
 def _call(name: str, device: torch.device, stream, *args, tail=()):
     """Run a C entry point with `device` current: name(*args, stream, *tail)."""
-    other = torch.cuda.current_device() != device.index
-    with torch.cuda.device(device) if other else contextlib.nullcontext():
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        _check(getattr(lib(), name)(*args, s.cuda_stream, *tail), name)
+    f = getattr(lib(), name)
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(device):
+            s = _raw_stream(index) if stream is None else stream.cuda_stream
+            code = f(*args, s, *tail)
+    else:
+        code = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream, *tail)
+    if code:
+        _check(code, name)
 
 
-def _tensor(t: torch.Tensor, name: str, device, dtype, shape=None, contiguous=True) -> int:
+def _cuda(t: torch.Tensor, name: str) -> torch.device:
+    """The device of the tensor that decides a call's."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
+    return t.device
+
+
+def _tensor(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
+    """Address of a contiguous tensor of this device, type and shape."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _dtype(t: torch.Tensor, name: str, allowed=(torch.bfloat16, torch.float16)) -> int:
-    if t.dtype not in allowed:
-        raise ValueError(f"{name} is {t.dtype}, expected one of {[str(d) for d in allowed]}")
-    return DTYPES[t.dtype]
+    d = t.dtype
+    if d not in allowed:
+        raise ValueError(f"{name} is {d}, expected one of {[str(x) for x in allowed]}")
+    return DTYPES[d]
 
 
-def _heads(t: torch.Tensor, name: str, device=None, dtype=None) -> _Heads:
+def _heads(t: torch.Tensor, name: str, device, dtype, shape=None) -> _Heads:
     """[T][H][D] rows of heads: any token and head strides, elements in a row."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens][heads][head_dim]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if t.dtype is not dtype or t.device != device or t.dim() != 3 or (shape is not None and t.shape != shape):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [tokens][heads][head_dim]")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    tok, head, one = t.stride()
+    if one != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return _Heads(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+    return _Heads(t.data_ptr(), t.shape[1], tok, head)
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _status(status, device) -> int | None:
@@ -133,15 +154,16 @@ def patch_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: s
     if n_pos < 1 or rot_dim < 2:
         raise PatchError(2, "patch_rope_table")
     table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
-    _call("patch_rope_table", table.device, stream, n_pos, rot_dim, ctypes.byref(cfg), table.data_ptr())
+    _call("patch_rope_table", table.device, stream, n_pos, rot_dim, _byref(cfg), table.data_ptr())
     return table
 
 
 def _table(table: torch.Tensor, device) -> tuple[int, int, int]:
     p = _tensor(table, "table", device, torch.float32)
-    if table.dim() != 3 or table.shape[2] != 2:
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
         raise ValueError("table must be [n_pos][rot_dim // 2][2] (patch_rope_table)")
-    return p, table.shape[0], 2 * table.shape[1]
+    return p, shape[0], 2 * shape[1]
 
 
 def _layout(layout: str) -> int:
@@ -161,32 +183,25 @@ def patch_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     backward=True turns the other way (times the table's amplitude): the
     gradient of the inputs from the gradient of the outputs.  Pass
     q_out=q, k_out=k to work in place."""
-    dev = q.device
-    hq = _heads(q, "q")
-    dt = _dtype(q, "q", tuple(DTYPES))
+    dev, dtype = _cuda(q, "q"), q.dtype
+    hq = _heads(q, "q", dev, dtype)
+    dt = _dtype(q, "q", DTYPES)
     T, _, D = q.shape
     tab, n_pos, rot = _table(table, dev)
     pos = _tensor(positions, "positions", dev, torch.int32, (T,))
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
-    ho = _heads(q_out, "q_out", dev, q.dtype)
+        q_out = _like(q)
+    ho = _byref(_heads(q_out, "q_out", dev, dtype, q.shape))
     hk = hko = None
     if k is not None:
-        hk = _heads(k, "k", dev, q.dtype)
-        if k.shape[0] != T or k.shape[2] != D:
-            raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        hk = _byref(_heads(k, "k", dev, dtype, (T, k.shape[1], D)))
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        elif k_out.shape != k.shape:
-            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
-        hko = _heads(k_out, "k_out", dev, q.dtype)
+            k_out = _like(k)
+        hko = _byref(_heads(k_out, "k_out", dev, dtype, k.shape))
     elif k_out is not None:
         raise ValueError("k_out without k")
-    ref = ctypes.byref
-    _call("patch_rope", dev, stream, ref(hq), ref(hk) if hk else None, ref(ho), ref(hko) if hko else None, T, D, dt,
-          pos, tab, n_pos, rot, _layout(layout), 1 if backward else 0, _status(status, dev))
+    _call("patch_rope", dev, stream, _byref(hq), hk, ho, hko, T, D, dt, pos, tab, n_pos, rot, _layout(layout),
+          1 if backward else 0, _status(status, dev))
     return q_out, k_out
 
 
@@ -203,13 +218,13 @@ class KvCache8:
     v_scale: torch.Tensor
 
     def struct(self) -> _Cache8:
-        k, s = self.k, self.k_scale
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        k = self.k
+        shape, f8, dev = k.shape, torch.float8_e4m3fn, k.device
+        if len(shape) != 4:
             raise ValueError("cache.k must be [n_pages][kv_heads][page][head_dim]")
-        n, h, page, d = k.shape
-        f8, dev = torch.float8_e4m3fn, k.device
-        return _Cache8(_tensor(k, "cache.k", dev, f8), _tensor(self.v, "cache.v", dev, f8, k.shape),
-                       _tensor(s, "cache.k_scale", dev, torch.float32, (n, h)),
+        n, h, page, d = shape
+        return _Cache8(_tensor(k, "cache.k", dev, f8), _tensor(self.v, "cache.v", dev, f8, shape),
+                       _tensor(self.k_scale, "cache.k_scale", dev, torch.float32, (n, h)),
                        _tensor(self.v_scale, "cache.v_scale", dev, torch.float32, (n, h)), n, h, page, d)
 
     @property
@@ -228,9 +243,10 @@ def new_kv_cache8(n_pages: int, kv_heads: int, page: int, head_dim: int, device=
 
 def _block_table(block_table: torch.Tensor, device) -> tuple[int, int, int]:
     p = _tensor(block_table, "block_table", device, torch.int32)
-    if block_table.dim() != 2:
+    shape = block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [batch][max_pages]")
-    return p, block_table.shape[0], block_table.shape[1]
+    return p, shape[0], shape[1]
 
 
 def patch_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache8, block_table: torch.Tensor,
@@ -242,19 +258,17 @@ def patch_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache8, block_ta
     cu_new[b + 1] - 1 (int32 [batch + 1]; None: one token each) at the positions
     that follow, in the pages of block_table (int32 [batch][max_pages]).  With a
     table (patch_rope_table) the keys are rotated to their positions on the way."""
-    dev = cache.k.device
+    dev, dtype = _cuda(cache.k, "cache.k"), k.dtype
     c = cache.struct()
-    hk = _heads(k, "k", dev)
-    hv = _heads(v, "v", dev, k.dtype)
     dt = _dtype(k, "k")
-    if k.shape != v.shape or k.shape[1:] != (c.kv_heads, c.head_dim):
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}, expected [tokens][{c.kv_heads}][{c.head_dim}]")
+    T = k.shape[0]
+    shape = (T, c.kv_heads, c.head_dim)
+    hk, hv = _heads(k, "k", dev, dtype, shape), _heads(v, "v", dev, dtype, shape)
     bt, batch, max_pages = _block_table(block_table, dev)
     past = _tensor(past_lens, "past_lens", dev, torch.int32, (batch,))
     cu = None if cu_new is None else _tensor(cu_new, "cu_new", dev, torch.int32, (batch + 1,))
     tab, n_pos, rot = (None, 0, 0) if table is None else _table(table, dev)
-    ref = ctypes.byref
-    _call("patch_kv8_append", dev, stream, ref(hk), ref(hv), k.shape[0], dt, ref(c), bt, max_pages, past, cu, batch,
+    _call("patch_kv8_append", dev, stream, _byref(hk), _byref(hv), T, dt, _byref(c), bt, max_pages, past, cu, batch,
           tab, n_pos, rot, _layout(layout), _status(status, dev))
 
 
@@ -278,28 +292,25 @@ def patch_attn_kv8(q: torch.Tensor, cache: KvCache8, block_table: torch.Tensor, 
     `window` of them.  A query that sees none gives zeros and lse -inf.  scale
     defaults to 1 / sqrt(D).  workspace: patch_attn_kv8_workspace_size bytes
     (uint8), zero-filled once, reusable by any later call on the same stream."""
-    dev = cache.k.device
+    dev, dtype = _cuda(cache.k, "cache.k"), q.dtype
     c = cache.struct()
-    hq = _heads(q, "q", dev)
+    hq = _heads(q, "q", dev, dtype)
     dt = _dtype(q, "q")
-    T, H, D = q.shape
+    T, H, D = shape = q.shape
     if D != c.head_dim or H % c.kv_heads:
         raise ValueError(f"q has {H} heads of {D}, the cache {c.kv_heads} of {c.head_dim}")
     bt, batch, max_pages = _block_table(block_table, dev)
     lens = _tensor(kv_lens, "kv_lens", dev, torch.int32, (batch,))
     cu = None if cu_q is None else _tensor(cu_q, "cu_q", dev, torch.int32, (batch + 1,))
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif out.shape != q.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    ho = _heads(out, "out", dev, q.dtype)
+        out = _like(q)
+    ho = _heads(out, "out", dev, dtype, shape)
     lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
     if workspace is None:
         workspace = torch.zeros(max(patch_attn_kv8_workspace_size(T, batch, H, cache), 16), dtype=torch.uint8, device=dev)
     ws = _tensor(workspace, "workspace", dev, torch.uint8)
-    ref = ctypes.byref
-    _call("patch_attn_kv8", dev, stream, ref(hq), T, dt, ref(c), bt, max_pages, lens, cu, batch,
-          1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, ref(ho),
+    _call("patch_attn_kv8", dev, stream, _byref(hq), T, dt, _byref(c), bt, max_pages, lens, cu, batch,
+          1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, _byref(ho),
           None if lse is None else lse.data_ptr(), ws, workspace.numel(), _status(status, dev), tail=(wait_limit_us,))
     return (out, lse) if want_lse else out
 
@@ -324,14 +335,15 @@ class Weight4:
         return 2 * self.codes.shape[1]
 
     def struct(self) -> _Weight4:
-        if self.group not in GROUPS4:
-            raise ValueError(f"group {self.group}, expected one of {GROUPS4}")
-        if self.codes.dim() != 2 or 2 * self.codes.shape[1] % self.group:
-            raise ValueError(f"codes must be [N][K / 2] with K a multiple of the group ({self.group})")
-        dev = self.codes.device
-        sd = _dtype(self.scales, "scales", tuple(DTYPES))
-        return _Weight4(self.N, self.K, self.group, sd, _tensor(self.codes, "codes", dev, torch.uint8),
-                        _tensor(self.scales, "scales", dev, self.scales.dtype, (self.N, self.K // self.group)))
+        codes, scales, group = self.codes, self.scales, self.group
+        if group not in GROUPS4:
+            raise ValueError(f"group {group}, expected one of {GROUPS4}")
+        shape = codes.shape
+        if len(shape) != 2 or 2 * shape[1] % group:
+            raise ValueError(f"codes must be [N][K / 2] with K a multiple of the group ({group})")
+        n, k, dev = shape[0], 2 * shape[1], codes.device
+        return _Weight4(n, k, group, _dtype(scales, "scales", DTYPES), _tensor(codes, "codes", dev, torch.uint8),
+                        _tensor(scales, "scales", dev, scales.dtype, (n, k // group)))
 
     @property
     def stored_bytes(self) -> int:
@@ -348,26 +360,26 @@ def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
         raise ValueError(f"group {group}: expected one of {GROUPS4} that divides K = {K}")
     if scale_dtype not in DTYPES:
         raise ValueError(f"scale_dtype {scale_dtype}, expected one of {[str(d) for d in DTYPES]}")
-    dev = W.device
+    dev = _cuda(W, "W")
     p = _tensor(W, "W", dev, W.dtype)
     w4 = Weight4(torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
                  torch.empty((N, K // group), dtype=scale_dtype, device=dev), group)
     st = w4.struct()
-    _call("patch_quantize4", dev, stream, p, _dtype(W, "W", tuple(DTYPES)), ctypes.byref(st))
+    _call("patch_quantize4", dev, stream, p, _dtype(W, "W", DTYPES), _byref(st))
     return w4
 
 
 def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X * W^T for up to 16 tokens (bf16 or fp16 [M][K]) and a 4-bit weight, fp32 sums."""
-    dev = weight.codes.device
+    dev, dtype = _cuda(weight.codes, "codes"), X.dtype
     st = weight.struct()
-    if X.dim() != 2 or X.shape[1] != st.K:
-        raise ValueError(f"X has shape {tuple(X.shape)}, weight has K={st.K}")
+    n, k = st.N, st.K
+    if X.dim() != 2 or X.shape[1] != k:
+        raise ValueError(f"X has shape {tuple(X.shape)}, weight has K={k}")
     M = X.shape[0]
     dt = _dtype(X, "X")
-    x = _tensor(X, "X", dev, X.dtype)
+    x = _tensor(X, "X", dev, dtype)
     if Y is None:
-        Y = torch.empty((M, st.N), dtype=X.dtype, device=dev)
-    y = _tensor(Y, "Y", dev, X.dtype, (M, st.N))
-    _call("patch_gemm4", dev, stream, x, M, dt, ctypes.byref(st), y)
+        Y = torch.empty((M, n), dtype=dtype, device=dev)
+    _call("patch_gemm4", dev, stream, x, M, dt, _byref(st), _tensor(Y, "Y", dev, dtype, (M, n)))
     return Y
