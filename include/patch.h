@@ -890,13 +890,14 @@ PATCH_API patch_status_t patch_quantize4(const void *W, int dtype, const patch_w
  * (16-byte aligned X), fp32 sums, one rounding.  No workspace; deterministic.
  * X enters the tensor cores as fp16, every 128 elements of a token divided by a
  * power of two first (elements below 2^-28 of the largest lose bits, less than
- * 2^-39 of it); a token with an infinity or NaN in it gives NaN.
+ * 2^-39 of it); a token with an infinity or NaN in it gives NaN.  A bounded wait
+ * (2 s) that runs out sets PATCH_DEV_TIMEOUT.  dev_status may be NULL.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, M outside 0 .. 16, group, dtypes),
  * PATCH_ERR_SHAPE (N < 1, K not a positive multiple of group, either > 2^30),
  * PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.  M == 0 is a no-op.
  */
 PATCH_API patch_status_t patch_gemm4(const void *X, int64_t M, int dtype, const patch_weight4 *W, void *Y,
-                                     void *stream);
+                                     int32_t *dev_status, void *stream);
 
 /*
  * patch_read_status: synchronise `stream`, copy *dev_status to *host_bits and

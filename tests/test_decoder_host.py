@@ -104,7 +104,7 @@ def test_weight4_refusals(lib):
         return ctypes.byref(dec._Weight4(N, K, group, sd, codes, scales))
 
     def gemm(x=F, M=2, dtype=0, weight=w(), y=F):
-        return lib.patch_gemm4(x, M, dtype, weight, y, None)
+        return lib.patch_gemm4(x, M, dtype, weight, y, None, None)
 
     assert gemm(M=0) == 0 and gemm(M=0, x=None, y=None) == 0
     for kw in (dict(M=-1), dict(M=17), dict(dtype=2), dict(weight=None), dict(x=None), dict(y=None),

@@ -269,7 +269,8 @@ patch_status_t patch_quantize4(const void* W, int dtype, const patch_weight4* ou
                                                                                                : PATCH_ERR_CUDA;
 }
 
-patch_status_t patch_gemm4(const void* X, int64_t M, int dtype, const patch_weight4* W, void* Y, void* stream) {
+patch_status_t patch_gemm4(const void* X, int64_t M, int dtype, const patch_weight4* W, void* Y,
+                           int32_t* dev_status, void* stream) {
   if (M < 0 || M > PATCH_DECODE_MAX_M || !half_type(dtype)) return PATCH_ERR_INVALID_ARG;
   patch_status_t st = check_weight4(W);
   if (st != PATCH_OK) return st;
@@ -279,7 +280,7 @@ patch_status_t patch_gemm4(const void* X, int64_t M, int dtype, const patch_weig
   int sms = 0;
   st = device_sms(&sms);
   if (st != PATCH_OK) return st;
-  return launch_gemm4(X, int(M), dtype, *W, Y, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_gemm4(X, int(M), dtype, *W, Y, dev_status, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PATCH_OK
              : PATCH_ERR_CUDA;
 }

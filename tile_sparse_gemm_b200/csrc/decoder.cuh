@@ -71,8 +71,8 @@ cudaError_t launch_attn_kv8(const AttnParams& P, int head_dim, int dtype, void* 
                             uint64_t limit_ns, cudaStream_t stream);
 
 cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out, int num_sms, cudaStream_t stream);
-cudaError_t launch_gemm4(const void* X, int M, int dtype, const patch_weight4& W, void* Y, int num_sms,
-                         cudaStream_t stream);
+cudaError_t launch_gemm4(const void* X, int M, int dtype, const patch_weight4& W, void* Y, int32_t* status,
+                         int num_sms, cudaStream_t stream);
 
 // ---- device helpers
 

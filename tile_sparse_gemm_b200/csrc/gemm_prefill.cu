@@ -668,6 +668,20 @@ bool make_map_2d_bf16_sw64(CUtensorMap* map, const void* base, uint64_t inner, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of bytes (pitch `inner`, a multiple of 16), boxes of box_inner x box_outer
+// bytes, 128-byte swizzle, zeros behind either end.
+bool make_map_rows_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int box_inner, int box_outer) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
+  const cuuint64_t strides[1] = {cuuint64_t(inner)};
+  const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Pages of a paged 8-bit cache: 3D map (element, token, page and head) over
 // [n_blocks][page][dim] bytes, boxes of `box` tokens of one block, swizzled by
 // the row's length (dim 64 or 128); a block behind the end reads as zeros.

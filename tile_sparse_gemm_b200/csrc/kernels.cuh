@@ -135,6 +135,8 @@ bool make_map_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64
 // The same with the 64-byte swizzle (box_inner <= 32 elements).
 bool make_map_2d_bf16_sw64(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                            uint32_t box_inner, uint32_t box_outer);
+// 2D byte map over rows of `inner` bytes (128-byte swizzle).
+bool make_map_rows_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int box_inner, int box_outer);
 // 3D byte map over a paged cache's blocks [n_blocks][page][dim], boxes of `box` tokens (dim 64 or 128, swizzled).
 bool make_map_pages_u8(CUtensorMap* map, const void* base, int64_t dim, int64_t page, int64_t n_blocks, int box);
 

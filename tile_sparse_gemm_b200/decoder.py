@@ -59,7 +59,7 @@ def signatures() -> dict:
         "patch_attn_kv8": [H, I64, I32, C, P, I64, P, P, I64, ctypes.c_float, I32, I64, H, P, P, SZ, P, P,
                            ctypes.c_uint64],
         "patch_quantize4": [P, I32, W, P],
-        "patch_gemm4": [P, I64, I32, W, P, P],
+        "patch_gemm4": [P, I64, I32, W, P, P, P],
     }
 
 
@@ -369,7 +369,8 @@ def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
     return w4
 
 
-def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X * W^T for up to 16 tokens (bf16 or fp16 [M][K]) and a 4-bit weight, fp32 sums."""
     dev, dtype = _cuda(weight.codes, "codes"), X.dtype
     st = weight.struct()
@@ -381,5 +382,6 @@ def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None,
     x = _tensor(X, "X", dev, dtype)
     if Y is None:
         Y = torch.empty((M, n), dtype=dtype, device=dev)
-    _call("patch_gemm4", dev, stream, x, M, dt, _byref(st), _tensor(Y, "Y", dev, dtype, (M, n)))
+    _call("patch_gemm4", dev, stream, x, M, dt, _byref(st), _tensor(Y, "Y", dev, dtype, (M, n)),
+          _status(status, dev))
     return Y
