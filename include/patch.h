@@ -865,7 +865,7 @@ PATCH_API patch_status_t patch_attn_kv8(const patch_heads *q, int64_t n_tokens, 
 /* A linear weight in 4 bits (host struct of device pointers):
  * W[n][k] = (code - 8) * scale[n][k / group], code 0 .. 15; codes u8 [N][K / 2],
  * the even k in the low half of a byte; scales [N][K / group] of scale_dtype
- * (PATCH_DTYPE_*).  group 32, 64 or 128, K a multiple of it; any N.  codes and
+ * (PATCH_DTYPE_BF16 or _FP16).  group 32, 64 or 128, K a multiple of it; any N.  codes and
  * scales 16-byte aligned.  A pruned (zero) weight is code 8 and stays exactly zero. */
 typedef struct {
     int64_t N, K;

@@ -108,7 +108,7 @@ def test_weight4_refusals(lib):
 
     assert gemm(M=0) == 0 and gemm(M=0, x=None, y=None) == 0
     for kw in (dict(M=-1), dict(M=17), dict(dtype=2), dict(weight=None), dict(x=None), dict(y=None),
-               dict(weight=w(group=16)), dict(weight=w(sd=3)), dict(weight=w(codes=None)), dict(weight=w(scales=None))):
+               dict(weight=w(group=16)), dict(weight=w(sd=2)), dict(weight=w(codes=None)), dict(weight=w(scales=None))):
         assert gemm(**kw) == 1, kw
     for kw in (dict(weight=w(N=0)), dict(weight=w(K=96)), dict(weight=w(K=0)), dict(weight=w(N=1 << 31))):
         assert gemm(**kw) == 2, kw
@@ -137,7 +137,7 @@ def test_binding_refuses_what_the_library_cannot_see():
         tsg.patch_attn_kv8(x, c, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         tsg.patch_quantize4(torch.zeros(4, 96), 64)
-    w = tsg.Weight4(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1), 64)
-    assert (w.N, w.K, w.stored_bytes) == (4, 64, 4 * 32 + 16)
+    w = tsg.Weight4(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.float16), 64)
+    assert (w.N, w.K, w.stored_bytes) == (4, 64, 4 * 32 + 8)
     with pytest.raises(ValueError):
         tsg.patch_gemm4(torch.zeros(1, 64, dtype=torch.bfloat16), w)

@@ -250,7 +250,7 @@ patch_status_t patch_attn_kv8(const patch_heads* q, int64_t n_tokens, int dtype,
 static patch_status_t check_weight4(const patch_weight4* W) {
   if (!W || !W->codes || !W->scales) return PATCH_ERR_INVALID_ARG;
   if (W->group != 32 && W->group != 64 && W->group != 128) return PATCH_ERR_INVALID_ARG;
-  if (W->scale_dtype != PATCH_DTYPE_FP32 && !half_type(W->scale_dtype)) return PATCH_ERR_INVALID_ARG;
+  if (!half_type(W->scale_dtype)) return PATCH_ERR_INVALID_ARG;
   if (W->N < 1 || W->K < 1 || W->K % W->group || W->N > kMaxCount || W->K > kMaxCount)
     return PATCH_ERR_SHAPE;
   if (!aligned16(W->codes) || !aligned16(W->scales)) return PATCH_ERR_ALIGN;

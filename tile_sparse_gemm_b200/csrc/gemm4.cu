@@ -34,17 +34,15 @@ __global__ void __launch_bounds__(256) quantize4_kernel(const T* __restrict__ W,
     const float s0 = __fdiv_rn(amax, 7.0f);
     const int64_t gi = i / lanes;
     const bool lead = (threadIdx.x & (lanes - 1)) == 0;
-    float s = s0;
+    float s;
     if (sdtype == PATCH_DTYPE_BF16) {
       const __nv_bfloat16 r = __float2bfloat16_rn(s0);
       s = to_f32(r);
       if (lead) static_cast<__nv_bfloat16*>(scales)[gi] = r;
-    } else if (sdtype == PATCH_DTYPE_FP16) {
+    } else {
       const __half r = __float2half_rn(s0);
       s = to_f32(r);
       if (lead) static_cast<__half*>(scales)[gi] = r;
-    } else if (lead) {
-      static_cast<float*>(scales)[gi] = s0;
     }
     uint32_t w = 0;
 #pragma unroll
@@ -91,43 +89,52 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // that brings their largest into [2^14, 2^15): bf16 and fp16 values down to 2^-28
 // of it stay exact, smaller ones are off by less than 2^-39 of it.
 //
-// A CTA takes 16 rows at a time; its warps take the blocks of 256 k in turn, 128
-// bytes of each row, fetched by TMA into a ring of the warp's own (no registers
-// held while bytes are on their way), and their sums are added in shared memory
-// in warp order (deterministic).  A lane reads 4 bytes at a time, so that the
-// four lanes of a row hold a quarter each of every group of 32.  Up to 8 tokens:
-// 8 warps, two CTAs per SM; up to 16: 16 warps, one CTA, whose X is twice as
-// large.  K beyond what fits is taken in slices, the sums kept in shared memory.
+// A CTA has an equal share of the row tiles of 16 and takes two at a time (a row
+// group); its warps take the group's blocks of 256 k in turn, 128 bytes of each
+// row, fetched by TMA into a ring of the warp's own (no registers held while bytes
+// are on their way), and their sums are added in shared memory in warp order
+// (deterministic).  A lane reads 4 bytes at a time, so that the four lanes of a
+// row hold a quarter each of every group of 32.  Up to 8 tokens: 8 warps, each
+// with both tiles (an operand of X serves two), two CTAs per SM.  Up to 16: 8
+// warps for either tile, one CTA per SM.  K beyond what X's place holds is taken
+// in slices, the sums of several row groups kept in shared memory.
+//
+// After the bytes, shared-memory passes bound it: an operand of X (16 bytes a
+// lane) costs a pass per 8 lanes; lanes of tokens beyond M load nothing.
 namespace g4 {
 
-constexpr int kBlockK = 256, kStageBytes = 16 * 128;
+constexpr int kBlockK = 256, kBoxBytes = 16 * 128;
 
 struct Params {
   CUtensorMap codes;
   const void *X, *scales;
   void* Y;
   int32_t* status;
-  int N, K, M, scale_dtype;
-  int blocks, slice_blocks, n_rb, rb_chunk;  // 256-k blocks of K and of a slice; row blocks, those of a CTA at a time
+  int N, K, M, dtype;
+  int blocks, slice_blocks, tiles, chunk;  // 256-k blocks of K and of a slice; row tiles; row groups of a CTA at a time
 };
+
+constexpr int kKWarps = 8;  // warps that share a row tile's blocks of k
+constexpr int kGroupRows = 32;
 
 template <int NT>
 struct Cfg {
-  static constexpr int kWarps = NT == 1 ? 8 : 16, kThreads = 32 * kWarps, kCtas = NT == 1 ? 2 : 1;
-  static constexpr int kStages = NT == 1 ? 3 : 2;
-  static constexpr int kBuffers = NT == 1 ? 2 : 1;       // of the warps' sums
-  static constexpr int kSum = 128 * NT;                  // outputs of a row block
-  static constexpr int kXBytes = NT == 1 ? 40960 : 132096;
-  static constexpr int kAccBytes = 7168;                 // of sums kept over slices
+  static constexpr int kRowWarps = NT, kWarps = kKWarps * kRowWarps, kThreads = 32 * kWarps, kCtas = NT == 1 ? 2 : 1;
+  static constexpr int MT = 2 / kRowWarps;                // row tiles of a warp
+  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStageBytes = MT * kBoxBytes;
+  static constexpr int kXBytes = NT == 1 ? 33280 : 66560;  // 2048 k of the most tokens
+  static constexpr int kKept = NT == 1 ? 4 : 8;           // row groups whose sums are kept over slices
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
 
-// Behind the ring: X [M][slice_blocks * 32 + 4] units of 16 bytes, sums per group, scales per 128 k, the warps' sums.
+// Behind the ring: X [M][slice_blocks * 32 + 4] units of 16 bytes, sums per group, scales per 128 k, the warps' sums
+// [warp][token][row of the group], sums kept over slices, a ring of scales beside that of codes.
 struct Layout {
-  int x, x_row, neg_sum, x_scale, reduce, acc, bars, bytes;
+  int x, x_row, neg_sum, x_scale, reduce, kept, scales, bars, bytes;
 };
 template <int NT, int GS>
-__host__ __device__ inline Layout layout(int M, int slice_blocks, int rb_chunk, bool slices) {
+__host__ __device__ inline Layout layout(int M, int slice_blocks, int chunk, bool slices) {
   using C = Cfg<NT>;
   Layout l;
   l.x = C::kRing;
@@ -135,21 +142,27 @@ __host__ __device__ inline Layout layout(int M, int slice_blocks, int rb_chunk, 
   l.neg_sum = l.x + M * l.x_row * 16;
   l.x_scale = l.neg_sum + slice_blocks * (kBlockK >> GS) * 8 * NT * 4;
   l.reduce = l.x_scale + slice_blocks * 2 * 8 * NT * 4;
-  l.acc = l.reduce + C::kBuffers * C::kWarps * C::kSum * 4;
-  l.bars = l.acc + (slices ? rb_chunk * C::kSum * 4 : 0);
+  l.kept = l.reduce + kKWarps * M * kGroupRows * 4;
+  l.scales = l.kept + (slices ? chunk * M * kGroupRows * 4 : 0);
+  l.bars = l.scales + C::kWarps * C::kStages * C::MT * 16 * (kBlockK >> GS) * 2;
   l.bytes = l.bars + C::kWarps * C::kStages * 8 + 16;
   return l;
 }
 
+__device__ __forceinline__ void store_y(uint16_t* at, float v, int dtype) {
+  *at = dtype == PATCH_DTYPE_BF16 ? f32_to_bf16_rne(v) : __half_as_ushort(__float2half_rn(v));
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+// where `on` is false v holds anything: a token beyond M, whose column is not stored
+__device__ __forceinline__ void lds128_if(bool on, uint32_t a, uint4& v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(a), "r"(uint32_t(on)));
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -168,22 +181,24 @@ __device__ __forceinline__ float f16_sum(uint32_t x) {
   return f.x + f.y;
 }
 
-// NT: 8-token tiles; GS: log2 of the group.
-template <typename T, int NT, int GS>
+// S: type of the scales; NT: 8-token tiles; GS: log2 of the group.
+template <typename S, int NT, int GS>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
   using C = Cfg<NT>;
-  constexpr int kWarps = C::kWarps, kStages = C::kStages;
-  constexpr int kGroups = kBlockK >> GS;              // of a block: 8, 4, 2
-  constexpr int kHeld = kGroups > 4 ? kGroups / 4 : 1;  // scales of a row that a lane loads
+  constexpr int kWarps = C::kWarps, kStages = C::kStages, MT = C::MT;
+  constexpr int kGroups = kBlockK >> GS;  // of a block: 8, 4, 2
+  constexpr int kScaleRow = 2 * kGroups;  // bytes of their scales
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q = lane & 3;
+  const int kw = warp % kKWarps, rw = warp / kKWarps;
   const bool slices = P.slice_blocks < P.blocks;
-  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.rb_chunk, slices);
+  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.chunk, slices);
   uint4* xs = reinterpret_cast<uint4*>(smem + L.x);
   float* neg_sum = reinterpret_cast<float*>(smem + L.neg_sum);
   float* x_scale = reinterpret_cast<float*>(smem + L.x_scale);
   float* reduce = reinterpret_cast<float*>(smem + L.reduce);
-  float* acc_kept = reinterpret_cast<float*>(smem + L.acc);
+  float* kept = reinterpret_cast<float*>(smem + L.kept);
+  uint8_t* scales = smem + L.scales + warp * kStages * MT * 16 * kScaleRow;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars) + warp * kStages;
   int* abort_flag = reinterpret_cast<int*>(smem + L.bars + kWarps * kStages * 8);
   if (lane == 0) {
@@ -197,87 +212,96 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // This CTA's row blocks are blockIdx.x + i gridDim.x, rb_chunk of them at a time; for
-  // these, slice after slice, the warp's blocks are warp, warp + kWarps, ... of the slice.
-  // The cursor of what is fetched next runs ahead through the same order.
+  // This CTA's row tiles are tile0 .. tile1 - 1, two of them a row group, `chunk` groups at a
+  // time; for these, slice after slice, the warp's blocks are kw, kw + kKWarps, ... of the
+  // slice.  The cursor of what is fetched next runs ahead through the same order.
+  const int tile0 = int(int64_t(P.tiles) * blockIdx.x / gridDim.x);
+  const int tile1 = int(int64_t(P.tiles) * (blockIdx.x + 1) / gridDim.x);
+  const int groups = (tile1 - tile0 + 1) / 2;
   struct Place {
-    int chunk0, b0, i, blk;  // first row block of the chunk, first block of the slice, row block of the chunk, block of the slice
+    int chunk0, b0, i, blk;  // first group of the chunk, first block of the slice, group of the chunk, block of the slice
   };
   auto nb_of = [&](int b0) { return min(P.slice_blocks, P.blocks - b0); };
-  auto valid = [&](const Place& p) { return p.chunk0 < P.n_rb; };
   // the next place with a block for this warp, from one whose block may lie behind the slice's last
   auto settle = [&](Place& p) {
-    while (valid(p) && p.blk >= nb_of(p.b0)) {
-      p.blk = warp;
-      if (++p.i >= P.rb_chunk || p.chunk0 + p.i * int(gridDim.x) >= P.n_rb) {
+    while (p.chunk0 < groups && p.blk >= nb_of(p.b0)) {
+      p.blk = kw;
+      if (++p.i >= P.chunk || p.chunk0 + p.i >= groups) {
         p.i = 0;
         p.b0 += P.slice_blocks;
         if (p.b0 >= P.blocks) {
           p.b0 = 0;
-          p.chunk0 += P.rb_chunk * gridDim.x;
+          p.chunk0 += P.chunk;
         }
       }
     }
   };
-  const uint32_t ring = tc::smem_u32(smem) + warp * kStages * kStageBytes;
-  Place fet = {int(blockIdx.x), 0, 0, warp};
+  const uint32_t ring = tc::smem_u32(smem) + warp * kStages * C::kStageBytes;
+  Place fet = {0, 0, 0, kw};
   settle(fet);
   int issued = 0, done = 0;
-  auto fetch = [&]() {
-    if (!valid(fet)) return;
-    const int st = issued % kStages;
-    if (lane == 0) {
-      tc::mbar_expect_tx(bars + st, kStageBytes);
-      tc::tma_load_2d(smem + warp * kStages * kStageBytes + st * kStageBytes, &P.codes, bars + st,
-                      (fet.b0 + fet.blk) * 128, (fet.chunk0 + fet.i * int(gridDim.x)) * 16);
+  const int row_groups = P.K >> GS;
+  const bool vec = P.K % kBlockK == 0;  // then a block's scales of a row are one aligned piece
+  auto fetch = [&]() {                  // the whole warp; one group of asynchronous copies a call, on every lane
+    if (fet.chunk0 < groups) {
+      const int st = issued % kStages, tile = tile0 + (fet.chunk0 + fet.i) * 2 + rw;
+      const int n_box = max(min(MT, tile1 - tile), 0);  // a last group may have one tile only: the other's sums are not stored
+      const int block = fet.b0 + fet.blk;
+      if (lane == 0) {
+        if (n_box > 0)
+          tc::mbar_expect_tx(bars + st, uint32_t(n_box * kBoxBytes));
+        else
+          tc::mbar_arrive(bars + st);
+        for (int b = 0; b < n_box; ++b)
+          tc::tma_load_2d(smem + (warp * kStages + st) * C::kStageBytes + b * kBoxBytes, &P.codes, bars + st, block * 128,
+                          (tile + b) * 16);
+      }
+      if (lane < 16 * MT) {  // a row's scales each
+        const int row = min(16 * tile + lane, P.N - 1);
+        const S* src = static_cast<const S*>(P.scales) + int64_t(row) * row_groups + block * kGroups;
+        S* dst = reinterpret_cast<S*>(scales + (st * MT * 16 + lane) * kScaleRow);
+        if (vec) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(kScaleRow)
+                       : "memory");
+        } else {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) dst[g] = block * kGroups + g < row_groups ? src[g] : from_f32<S>(0.0f);
+        }
+      }
+      ++issued;
+      fet.blk += kKWarps;
+      settle(fet);
     }
-    ++issued;
-    fet.blk += kWarps;
-    settle(fet);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (int s = 0; s < kStages; ++s) fetch();
 
-  const int row_groups = P.K >> GS;
-  // scales as stored, of rows 16 rb + n and + 8, this lane's groups of a block
-  auto load_scales = [&](uint32_t (&s)[2][kHeld], int rb, int block) {
+  uint32_t x_lane[NT];
+  bool has_x[NT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t at = int64_t(min(16 * rb + n + 8 * h, P.N - 1)) * row_groups;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int g = block * kGroups + 4 * i + (q & (kGroups - 1));
-        s[h][i] = 0;
-        if (g < row_groups)
-          s[h][i] = P.scale_dtype == PATCH_DTYPE_FP32 ? static_cast<const uint32_t*>(P.scales)[at + g]
-                                                      : static_cast<const uint16_t*>(P.scales)[at + g];
-      }
-    }
-  };
-  auto scale_of = [&](uint32_t raw) {  // times 2^12
-    const float s = P.scale_dtype == PATCH_DTYPE_BF16   ? __uint_as_float(raw << 16)
-                    : P.scale_dtype == PATCH_DTYPE_FP16 ? __half2float(__ushort_as_half(uint16_t(raw)))
-                                                        : __uint_as_float(raw);
-    return s * 4096.0f;
-  };
-  uint32_t x_lane[NT];  // tokens beyond M read the last one's X: their columns are not stored
-#pragma unroll
-  for (int t = 0; t < NT; ++t) x_lane[t] = tc::smem_u32(xs) + uint32_t(min(8 * t + n, P.M - 1) * L.x_row + q) * 16;
+  for (int t = 0; t < NT; ++t) {
+    has_x[t] = 8 * t + n < P.M;
+    x_lane[t] = tc::smem_u32(xs) + uint32_t(min(8 * t + n, P.M - 1) * L.x_row + q) * 16;
+  }
   // the lane's words: row n, chunk c of 16 bytes at c ^ n (128-byte swizzle); row n + 8 is 1024 bytes on
   const uint32_t word0 = ring + n * 128 + n * 16 + 4 * q;
 
-  int parity = 0;
-  for (int chunk0 = blockIdx.x; chunk0 < P.n_rb; chunk0 += gridDim.x * P.rb_chunk) {
+  for (int chunk0 = 0; chunk0 < groups; chunk0 += P.chunk) {
     for (int b0 = 0; b0 < P.blocks; b0 += P.slice_blocks) {
       const int nb = nb_of(b0);
       // ---- X of the slice: 16 threads per token and 128 k
-      if (slices || chunk0 == int(blockIdx.x)) {
+      if (slices || chunk0 == 0) {
         __syncthreads();  // the last slice's is read
         for (int u = threadIdx.x; u < P.M * nb * 32; u += C::kThreads) {
           const int half_blk = (u >> 4) % (2 * nb), m = (u >> 4) / (2 * nb), p = u & 15;
           const int k = b0 * kBlockK + half_blk * 128 + 8 * p;
           float x[8];
           if (k < P.K) {
-            load16(static_cast<const T*>(P.X) + int64_t(m) * P.K + k, x);
+            const uint16_t* src = static_cast<const uint16_t*>(P.X) + int64_t(m) * P.K + k;
+            if (P.dtype == PATCH_DTYPE_BF16)
+              load16(reinterpret_cast<const __nv_bfloat16*>(src), x);
+            else
+              load16(reinterpret_cast<const __half*>(src), x);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = 0.0f;
@@ -307,94 +331,113 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
         __syncthreads();
       }
 
-      for (int i_rb = 0; i_rb < P.rb_chunk; ++i_rb) {
-        const int rb = chunk0 + i_rb * gridDim.x;
-        if (rb >= P.n_rb) break;
-        float y[NT][4];
+      for (int i = 0; i < P.chunk && chunk0 + i < groups; ++i) {
+        const int row0 = 16 * (tile0 + (chunk0 + i) * 2);
+        float y[MT][NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[t][i] = 0.0f;
-        uint32_t raw[2][kHeld];
-        if (warp < nb) load_scales(raw, rb, b0 + warp);
-        for (int blk = warp; blk < nb; blk += kWarps) {
+          for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[t][u][k] = 0.0f;
+        for (int blk = kw; blk < nb; blk += kKWarps) {
           const int st = done % kStages;
           const bool ok = tc::wait_bounded(bars + st, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, false);
           ++done;
           if (!__all_sync(0xFFFFFFFFu, ok)) break;
-          float s[2][kHeld];
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");  // this stage's scales
+          __syncwarp();
+          alignas(16) S sc[MT][2][kGroups];  // of rows n and n + 8
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) s[h][i] = scale_of(raw[h][i]);
-          if (blk + kWarps < nb) load_scales(raw, rb, b0 + blk + kWarps);
-          const uint32_t words = word0 + st * kStageBytes;
-          const int x_at = blk * 512;
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* at = scales + ((st * MT + t) * 16 + n + 8 * h) * kScaleRow;
+              if constexpr (kScaleRow == 16) *reinterpret_cast<uint4*>(sc[t][h]) = *reinterpret_cast<const uint4*>(at);
+              if constexpr (kScaleRow == 8) *reinterpret_cast<uint2*>(sc[t][h]) = *reinterpret_cast<const uint2*>(at);
+              if constexpr (kScaleRow == 4) *reinterpret_cast<uint32_t*>(sc[t][h]) = *reinterpret_cast<const uint32_t*>(at);
+            }
+          const uint32_t words = word0 + st * C::kStageBytes;
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {  // 128 k
             constexpr int kPer = 1 << (GS - 5);  // chunks of 32 k in a group
-            float sum[NT][4], acc[NT][4];
+            float sum[MT][NT][4], acc[MT][NT][4];
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) {
               const int c = 4 * hb + c4;
-              const uint32_t a0 = lds32(words ^ (c << 4)), a1 = lds32((words ^ (c << 4)) + 1024);
-              const uint32_t r0 = a0 >> 8, r1 = a1 >> 8;
+              uint4 x[NT];
 #pragma unroll
-              for (int t = 0; t < NT; ++t) {
+              for (int u = 0; u < NT; ++u) {
+                lds128_if(has_x[u], x_lane[u] + (blk * 8 + c) * 64, x[u]);
                 if (c4 % kPer == 0) {
-                  const float2 neg = *reinterpret_cast<const float2*>(neg_sum + ((blk * 8 + c) / kPer * NT + t) * 8 + 2 * q);
-                  acc[t][0] = acc[t][2] = neg.x;
-                  acc[t][1] = acc[t][3] = neg.y;
-                }
-                const uint4 x = lds128(x_lane[t] + x_at + 64 * c);
-                mma(acc[t], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u, a1 & 0x00F000F0u, x.x, x.y);
-                mma(acc[t], r0 & 0x000F000Fu, r1 & 0x000F000Fu, r0 & 0x00F000F0u, r1 & 0x00F000F0u, x.z, x.w);
-              }
-              if (c4 % kPer == kPer - 1) {  // the group's scales, from the lane that loaded them
-                const int g = c / kPer;
-                const float s0 = __shfl_sync(0xFFFFFFFFu, s[0][g >> 2], (lane & ~3) | (g & 3));
-                const float s1 = __shfl_sync(0xFFFFFFFFu, s[1][g >> 2], (lane & ~3) | (g & 3));
+                  const float2 neg = *reinterpret_cast<const float2*>(neg_sum + ((blk * 8 + c) / kPer * NT + u) * 8 + 2 * q);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float f = i < 2 ? s0 : s1;
-                    sum[t][i] = c4 == kPer - 1 ? acc[t][i] * f : fmaf(acc[t][i], f, sum[t][i]);
+                  for (int t = 0; t < MT; ++t) {
+                    acc[t][u][0] = acc[t][u][2] = neg.x;
+                    acc[t][u][1] = acc[t][u][3] = neg.y;
                   }
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                const uint32_t at = (words ^ (c << 4)) + t * kBoxBytes;
+                const uint32_t a0 = lds32(at), a1 = lds32(at + 1024);
+                const uint32_t r0 = a0 >> 8, r1 = a1 >> 8;
+#pragma unroll
+                for (int u = 0; u < NT; ++u) {
+                  mma(acc[t][u], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u, a1 & 0x00F000F0u, x[u].x, x[u].y);
+                  mma(acc[t][u], r0 & 0x000F000Fu, r1 & 0x000F000Fu, r0 & 0x00F000F0u, r1 & 0x00F000F0u, x[u].z, x[u].w);
+                }
+                if (c4 % kPer == kPer - 1) {
+                  const int g = c / kPer;
+                  const float s0 = to_f32(sc[t][0][g]), s1 = to_f32(sc[t][1][g]);
+#pragma unroll
+                  for (int u = 0; u < NT; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const float f = k < 2 ? s0 : s1;
+                      sum[t][u][k] = c4 == kPer - 1 ? acc[t][u][k] * f : fmaf(acc[t][u][k], f, sum[t][u][k]);
+                    }
+                }
               }
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const float2 f = *reinterpret_cast<const float2*>(x_scale + ((blk * 2 + hb) * NT + t) * 8 + 2 * q);
+            for (int u = 0; u < NT; ++u) {
+              const float2 f = *reinterpret_cast<const float2*>(x_scale + ((blk * 2 + hb) * NT + u) * 8 + 2 * q);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) y[t][i] = fmaf(sum[t][i], i & 1 ? f.y : f.x, y[t][i]);
+              for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[t][u][k] = fmaf(sum[t][u][k], k & 1 ? f.y : f.x, y[t][u][k]);
             }
           }
           __syncwarp();  // every lane has read the stage
           fetch();
         }
-        // ---- add the warps' sums: [warp][token][row]
-        if (C::kBuffers == 1) __syncthreads();  // the last ones are read
-        float* buf = reduce + parity * kWarps * C::kSum;
-        if (C::kBuffers == 2) parity ^= 1;
+        // ---- add the warps' sums: [kw][token][row of the group]
+        const int outs = P.M * kGroupRows;
+        __syncthreads();  // the last ones are read
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            buf[warp * C::kSum + (8 * t + 2 * q + (i & 1)) * 16 + n + 8 * (i >> 1)] = y[t][i];
+          for (int k = 0; k < 4; ++k) {
+            const int m = 8 * u + 2 * q + (k & 1);
+            if (m < P.M)
+#pragma unroll
+              for (int t = 0; t < MT; ++t)
+                reduce[kw * outs + m * kGroupRows + 16 * (rw + t) + n + 8 * (k >> 1)] = y[t][u][k];
+          }
         __syncthreads();
-        const int o = threadIdx.x;  // output: token o / 16, row o % 16
-        if (o < C::kSum && (o >> 4) < P.M) {
+        for (int o = threadIdx.x; o < outs; o += C::kThreads) {
           float v = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += buf[w * C::kSum + o];
+          for (int w = 0; w < kKWarps; ++w) v += reduce[w * outs + o];
           if (slices) {
-            float* kept = acc_kept + i_rb * C::kSum + o;
-            if (b0 > 0) v += *kept;
-            *kept = v;
+            if (b0 > 0) v += kept[i * outs + o];
+            kept[i * outs + o] = v;
           }
-          const int row = 16 * rb + (o & 15);
-          if (b0 + nb == P.blocks && row < P.N) static_cast<T*>(P.Y)[int64_t(o >> 4) * P.N + row] = from_f32<T>(v);
+          const int row = row0 + o % kGroupRows;
+          if (b0 + nb == P.blocks && row < P.N && row < 16 * tile1)
+            store_y(static_cast<uint16_t*>(P.Y) + int64_t(o / kGroupRows) * P.N + row, v * 4096.0f, P.dtype);
         }
       }
     }
@@ -404,30 +447,30 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
     tc::wait_bounded(bars + done % kStages, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, true);
 }
 
-template <typename T, int NT, int GS>
+template <typename S, int NT, int GS>
 static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   using C = Cfg<NT>;
-  P.n_rb = (P.N + 15) / 16;
+  P.tiles = (P.N + 15) / 16;
   P.blocks = (P.K + kBlockK - 1) / kBlockK;
-  const int grid = P.n_rb < C::kCtas * num_sms ? P.n_rb : C::kCtas * num_sms;
-  const int per_cta = (P.n_rb + grid - 1) / grid;
+  const int grid = P.tiles < C::kCtas * num_sms ? P.tiles : C::kCtas * num_sms;
+  const int per_cta = ((P.tiles + grid - 1) / grid + 1) / 2;
   // a slice: whole rounds of the warps, as many as fit
-  const int fit = (C::kXBytes / P.M - 64) / (kBlockK * 2) / C::kWarps * C::kWarps;
+  const int fit = (C::kXBytes / P.M - 64) / (kBlockK * 2) / kKWarps * kKWarps;
   const bool slices = P.blocks > fit;
   P.slice_blocks = slices ? fit : P.blocks;
-  P.rb_chunk = slices && per_cta > C::kAccBytes / (C::kSum * 4) ? C::kAccBytes / (C::kSum * 4) : per_cta;
-  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.rb_chunk, slices);
-  auto kernel = gemm4_kernel<T, NT, GS>;
+  P.chunk = slices && per_cta > C::kKept ? C::kKept : per_cta;
+  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.chunk, slices);
+  auto kernel = gemm4_kernel<S, NT, GS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(unsigned(grid)), dim3(C::kThreads), size_t(L.bytes), stream, P);
 }
 
-template <typename T, int NT>
+template <typename S, int NT>
 static cudaError_t launch_group(const Params& P, int group, int num_sms, cudaStream_t stream) {
-  if (group == 32) return launch<T, NT, 5>(P, num_sms, stream);
-  if (group == 64) return launch<T, NT, 6>(P, num_sms, stream);
-  return launch<T, NT, 7>(P, num_sms, stream);
+  if (group == 32) return launch<S, NT, 5>(P, num_sms, stream);
+  if (group == 64) return launch<S, NT, 6>(P, num_sms, stream);
+  return launch<S, NT, 7>(P, num_sms, stream);
 }
 
 }  // namespace g4
@@ -442,10 +485,10 @@ cudaError_t launch_gemm4(const void* X, int M, int dtype, const patch_weight4& W
   P.N = int(W.N);
   P.K = int(W.K);
   P.M = M;
-  P.scale_dtype = W.scale_dtype;
+  P.dtype = dtype;
   if (!make_map_rows_u8(&P.codes, W.codes, W.K / 2, W.N, 128, 16)) return cudaErrorInvalidValue;
   using BF = __nv_bfloat16;
-  if (dtype == PATCH_DTYPE_BF16)
+  if (W.scale_dtype == PATCH_DTYPE_BF16)
     return M <= 8 ? g4::launch_group<BF, 1>(P, W.group, num_sms, stream) : g4::launch_group<BF, 2>(P, W.group, num_sms, stream);
   return M <= 8 ? g4::launch_group<__half, 1>(P, W.group, num_sms, stream)
                 : g4::launch_group<__half, 2>(P, W.group, num_sms, stream);

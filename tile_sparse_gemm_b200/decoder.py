@@ -323,7 +323,7 @@ class Weight4:
     """A linear weight in 4 bits: W[n][k] = (code - 8) * scales[n][k // group], codes
     u8 [N][K // 2] with the even k in the low half of a byte."""
     codes: torch.Tensor
-    scales: torch.Tensor  # bf16, fp16 or fp32 [N][K // group]
+    scales: torch.Tensor  # bf16 or fp16 [N][K // group]
     group: int
 
     @property
@@ -342,7 +342,7 @@ class Weight4:
         if len(shape) != 2 or 2 * shape[1] % group:
             raise ValueError(f"codes must be [N][K / 2] with K a multiple of the group ({group})")
         n, k, dev = shape[0], 2 * shape[1], codes.device
-        return _Weight4(n, k, group, _dtype(scales, "scales", DTYPES), _tensor(codes, "codes", dev, torch.uint8),
+        return _Weight4(n, k, group, _dtype(scales, "scales"), _tensor(codes, "codes", dev, torch.uint8),
                         _tensor(scales, "scales", dev, scales.dtype, (n, k // group)))
 
     @property
@@ -358,8 +358,8 @@ def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
     N, K = W.shape
     if group not in GROUPS4 or K % group:
         raise ValueError(f"group {group}: expected one of {GROUPS4} that divides K = {K}")
-    if scale_dtype not in DTYPES:
-        raise ValueError(f"scale_dtype {scale_dtype}, expected one of {[str(d) for d in DTYPES]}")
+    if scale_dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"scale_dtype {scale_dtype}, expected torch.bfloat16 or torch.float16")
     dev = _cuda(W, "W")
     p = _tensor(W, "W", dev, W.dtype)
     w4 = Weight4(torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
