@@ -97,7 +97,7 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // row hold a quarter each of every group of 32.  Up to 8 tokens: 8 warps, each
 // with both tiles (an operand of X serves two), two CTAs per SM.  Up to 16: 8
 // warps for either tile, one CTA per SM.  K beyond what X's place holds is taken
-// in slices, the sums of several row groups kept in shared memory.
+// in slices, the sums of four row groups kept meanwhile by the threads that add them.
 //
 // After the bytes, shared-memory passes bound it: an operand of X (16 bytes a
 // lane) costs a pass per 8 lanes; lanes of tokens beyond M load nothing.
@@ -116,34 +116,33 @@ struct Params {
 
 constexpr int kKWarps = 8;  // warps that share a row tile's blocks of k
 constexpr int kGroupRows = 32;
+constexpr int kKept = 4;  // row groups whose sums are kept over slices, in registers
 
 template <int NT>
 struct Cfg {
   static constexpr int kRowWarps = NT, kWarps = kKWarps * kRowWarps, kThreads = 32 * kWarps, kCtas = NT == 1 ? 2 : 1;
   static constexpr int MT = 2 / kRowWarps;                // row tiles of a warp
-  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStages = 2;
   static constexpr int kStageBytes = MT * kBoxBytes;
-  static constexpr int kXBytes = NT == 1 ? 33280 : 66560;  // 2048 k of the most tokens
-  static constexpr int kKept = NT == 1 ? 4 : 8;           // row groups whose sums are kept over slices
+  static constexpr int kXBytes = NT == 1 ? 32768 : 131072;  // 2048 or 4096 k of the most tokens
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
 
-// Behind the ring: X [M][slice_blocks * 32 + 4] units of 16 bytes, sums per group, scales per 128 k, the warps' sums
-// [warp][token][row of the group], sums kept over slices, a ring of scales beside that of codes.
+// Behind the ring: X [M][slice_blocks * 32] units of 16 bytes, sums per group, scales per 128 k, the warps' sums
+// [warp][token][row of the group], a ring of scales beside that of codes.
 struct Layout {
-  int x, x_row, neg_sum, x_scale, reduce, kept, scales, bars, bytes;
+  int x, x_row, neg_sum, x_scale, reduce, scales, bars, bytes;
 };
 template <int NT, int GS>
-__host__ __device__ inline Layout layout(int M, int slice_blocks, int chunk, bool slices) {
+__host__ __device__ inline Layout layout(int M, int slice_blocks) {
   using C = Cfg<NT>;
   Layout l;
   l.x = C::kRing;
-  l.x_row = slice_blocks * 32 + 4;  // 64 bytes beyond a multiple of 128: 8 tokens' pieces lie in different banks
+  l.x_row = slice_blocks * 32;
   l.neg_sum = l.x + M * l.x_row * 16;
   l.x_scale = l.neg_sum + slice_blocks * (kBlockK >> GS) * 8 * NT * 4;
   l.reduce = l.x_scale + slice_blocks * 2 * 8 * NT * 4;
-  l.kept = l.reduce + kKWarps * M * kGroupRows * 4;
-  l.scales = l.kept + (slices ? chunk * M * kGroupRows * 4 : 0);
+  l.scales = l.reduce + kKWarps * M * kGroupRows * 4;
   l.bars = l.scales + C::kWarps * C::kStages * C::MT * 16 * (kBlockK >> GS) * 2;
   l.bytes = l.bars + C::kWarps * C::kStages * 8 + 16;
   return l;
@@ -164,12 +163,13 @@ __device__ __forceinline__ void lds128_if(bool on, uint32_t a, uint4& v) {
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
       : "r"(a), "r"(uint32_t(on)));
 }
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+// d = a b + c
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, const float (&c)[4]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -192,12 +192,11 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q = lane & 3;
   const int kw = warp % kKWarps, rw = warp / kKWarps;
   const bool slices = P.slice_blocks < P.blocks;
-  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.chunk, slices);
+  const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   uint4* xs = reinterpret_cast<uint4*>(smem + L.x);
   float* neg_sum = reinterpret_cast<float*>(smem + L.neg_sum);
   float* x_scale = reinterpret_cast<float*>(smem + L.x_scale);
   float* reduce = reinterpret_cast<float*>(smem + L.reduce);
-  float* kept = reinterpret_cast<float*>(smem + L.kept);
   uint8_t* scales = smem + L.scales + warp * kStages * MT * 16 * kScaleRow;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars) + warp * kStages;
   int* abort_flag = reinterpret_cast<int*>(smem + L.bars + kWarps * kStages * 8);
@@ -218,120 +217,146 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   const int tile0 = int(int64_t(P.tiles) * blockIdx.x / gridDim.x);
   const int tile1 = int(int64_t(P.tiles) * (blockIdx.x + 1) / gridDim.x);
   const int groups = (tile1 - tile0 + 1) / 2;
-  struct Place {
-    int chunk0, b0, i, blk;  // first group of the chunk, first block of the slice, group of the chunk, block of the slice
-  };
   auto nb_of = [&](int b0) { return min(P.slice_blocks, P.blocks - b0); };
-  // the next place with a block for this warp, from one whose block may lie behind the slice's last
-  auto settle = [&](Place& p) {
-    while (p.chunk0 < groups && p.blk >= nb_of(p.b0)) {
-      p.blk = kw;
-      if (++p.i >= P.chunk || p.chunk0 + p.i >= groups) {
-        p.i = 0;
-        p.b0 += P.slice_blocks;
-        if (p.b0 >= P.blocks) {
-          p.b0 = 0;
-          p.chunk0 += P.chunk;
-        }
-      }
-    }
-  };
-  const uint32_t ring = tc::smem_u32(smem) + warp * kStages * C::kStageBytes;
-  Place fet = {0, 0, 0, kw};
-  settle(fet);
-  int issued = 0, done = 0;
   const int row_groups = P.K >> GS;
   const bool vec = P.K % kBlockK == 0;  // then a block's scales of a row are one aligned piece
-  auto fetch = [&]() {                  // the whole warp; one group of asynchronous copies a call, on every lane
+  struct {
+    int chunk0, b0, i, blk;  // first group of the chunk, first block of the slice, group of the chunk, block of the slice
+    int nb, tile, boxes;     // blocks of the slice, the warp's first tile and how many it has
+    const S* src;            // this lane's row's scales of block b0
+  } fet = {0, 0, 0, kw, 0, 0, 0, nullptr};
+  auto settle = [&](bool next) {  // the first place with a block for this warp, from here or from the next group on
+    for (;; next = true) {
+      if (next) {
+        fet.blk = kw;
+        if (!slices && fet.chunk0 + fet.i + 2 < groups) {  // the common case: the next group, of two whole tiles
+          ++fet.i;
+          fet.tile += 2;
+          fet.src += int64_t(2 * 16) * row_groups;
+          return;
+        }
+        if (++fet.i >= P.chunk || fet.chunk0 + fet.i >= groups) {
+          fet.i = 0;
+          fet.b0 += P.slice_blocks;
+          if (fet.b0 >= P.blocks) {
+            fet.b0 = 0;
+            fet.chunk0 += P.chunk;
+          }
+        }
+      }
+      if (fet.chunk0 >= groups) return;
+      fet.nb = nb_of(fet.b0);
+      if (fet.blk < fet.nb) break;
+    }
+    fet.tile = tile0 + (fet.chunk0 + fet.i) * 2 + rw;
+    fet.boxes = max(min(MT, tile1 - fet.tile), 0);  // a last group may have one tile only: the other's sums are not stored
+    fet.src = static_cast<const S*>(P.scales) + int64_t(min(16 * fet.tile + lane, P.N - 1)) * row_groups + fet.b0 * kGroups;
+  };
+  const uint32_t ring = tc::smem_u32(smem) + warp * kStages * C::kStageBytes;
+  settle(false);
+  int issued = 0, done = 0;
+  auto fetch = [&]() {  // the whole warp; one group of asynchronous copies a call, on every lane
     if (fet.chunk0 < groups) {
-      const int st = issued % kStages, tile = tile0 + (fet.chunk0 + fet.i) * 2 + rw;
-      const int n_box = max(min(MT, tile1 - tile), 0);  // a last group may have one tile only: the other's sums are not stored
-      const int block = fet.b0 + fet.blk;
+      const int st = issued % kStages;
       if (lane == 0) {
-        if (n_box > 0)
-          tc::mbar_expect_tx(bars + st, uint32_t(n_box * kBoxBytes));
+        if (fet.boxes > 0)
+          tc::mbar_expect_tx(bars + st, uint32_t(fet.boxes * kBoxBytes));
         else
           tc::mbar_arrive(bars + st);
-        for (int b = 0; b < n_box; ++b)
-          tc::tma_load_2d(smem + (warp * kStages + st) * C::kStageBytes + b * kBoxBytes, &P.codes, bars + st, block * 128,
-                          (tile + b) * 16);
+        uint8_t* dst = smem + (warp * kStages + st) * C::kStageBytes;
+        const int x = (fet.b0 + fet.blk) * 128;
+        if (fet.boxes > 0) tc::tma_load_2d(dst, &P.codes, bars + st, x, fet.tile * 16);
+        if (fet.boxes > 1) tc::tma_load_2d(dst + kBoxBytes, &P.codes, bars + st, x, fet.tile * 16 + 16);
       }
       if (lane < 16 * MT) {  // a row's scales each
-        const int row = min(16 * tile + lane, P.N - 1);
-        const S* src = static_cast<const S*>(P.scales) + int64_t(row) * row_groups + block * kGroups;
+        const S* src = fet.src + fet.blk * kGroups;
         S* dst = reinterpret_cast<S*>(scales + (st * MT * 16 + lane) * kScaleRow);
         if (vec) {
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(kScaleRow)
                        : "memory");
         } else {
+          const int left = row_groups - (fet.b0 + fet.blk) * kGroups;
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) dst[g] = block * kGroups + g < row_groups ? src[g] : from_f32<S>(0.0f);
+          for (int g = 0; g < kGroups; ++g) dst[g] = g < left ? src[g] : from_f32<S>(0.0f);
         }
       }
       ++issued;
       fet.blk += kKWarps;
-      settle(fet);
+      if (fet.blk >= fet.nb) settle(true);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (int s = 0; s < kStages; ++s) fetch();
 
-  uint32_t x_lane[NT];
+  uint32_t x_lane[NT][2];  // of even and odd chunks
   bool has_x[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     has_x[t] = 8 * t + n < P.M;
-    x_lane[t] = tc::smem_u32(xs) + uint32_t(min(8 * t + n, P.M - 1) * L.x_row + q) * 16;
+    const int m = min(8 * t + n, P.M - 1);
+    x_lane[t][0] = tc::smem_u32(xs) + uint32_t(m * L.x_row + q) * 16 + (m & 1) * 64;
+    x_lane[t][1] = x_lane[t][0] - (m & 1) * 128;
   }
   // the lane's words: row n, chunk c of 16 bytes at c ^ n (128-byte swizzle); row n + 8 is 1024 bytes on
   const uint32_t word0 = ring + n * 128 + n * 16 + 4 * q;
 
+  float kept[kKept] = {};
   for (int chunk0 = 0; chunk0 < groups; chunk0 += P.chunk) {
     for (int b0 = 0; b0 < P.blocks; b0 += P.slice_blocks) {
       const int nb = nb_of(b0);
       // ---- X of the slice: 16 threads per token and 128 k
       if (slices || chunk0 == 0) {
         __syncthreads();  // the last slice's is read
-        for (int u = threadIdx.x; u < P.M * nb * 32; u += C::kThreads) {
-          const int half_blk = (u >> 4) % (2 * nb), m = (u >> 4) / (2 * nb), p = u & 15;
-          const int k = b0 * kBlockK + half_blk * 128 + 8 * p;
-          float x[8];
-          if (k < P.K) {
-            const uint16_t* src = static_cast<const uint16_t*>(P.X) + int64_t(m) * P.K + k;
-            if (P.dtype == PATCH_DTYPE_BF16)
-              load16(reinterpret_cast<const __nv_bfloat16*>(src), x);
-            else
-              load16(reinterpret_cast<const __half*>(src), x);
-          } else {
+        constexpr int kAhead = 4;  // units of 8 elements a thread has under way
+        const int units = P.M * nb * 32;
+        for (int u0 = threadIdx.x; u0 < units; u0 += kAhead * C::kThreads) {
+          uint4 raw[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * C::kThreads, m = u / (nb * 32), k = b0 * kBlockK + (u - m * nb * 32) * 8;
+            raw[j] = make_uint4(0, 0, 0, 0);
+            if (u < units && k < P.K)
+              raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.X) + int64_t(m) * P.K + k);
           }
-          float amax = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-          const unsigned half = 0xFFFFu << (threadIdx.x & 16);  // these 16 threads leave the loop together
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * C::kThreads;
+            if (u >= units) break;  // all 16 threads of a token's 128 k together
+            const int m = u / (nb * 32), p = u & 15, half_blk = (u - m * nb * 32) >> 4;
+            float x[8];
+            if (P.dtype == PATCH_DTYPE_BF16)
+              load16(reinterpret_cast<const __nv_bfloat16*>(&raw[j]), x);
+            else
+              load16(reinterpret_cast<const __half*>(&raw[j]), x);
+            float amax = 0.0f;
 #pragma unroll
-          for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
-          const int e = max(int(__float_as_uint(amax) >> 23) - 127, -113);
-          const float f = e == 128 ? 1.0f : pow2i(14 - e);
-          uint4 v;
-          v.x = pack_f16(x[0] * f, x[4] * f);
-          v.y = pack_f16(x[1] * f * 0.0625f, x[5] * f * 0.0625f);
-          v.z = pack_f16(x[2] * f, x[6] * f);
-          v.w = pack_f16(x[3] * f * 0.0625f, x[7] * f * 0.0625f);
-          xs[m * L.x_row + 16 * half_blk + p] = v;
-          float sum = f16_sum(v.x) + f16_sum(v.z) + 16.0f * (f16_sum(v.y) + f16_sum(v.w));
-          constexpr int kLanes = 1 << (GS - 3);  // of a group
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+            const unsigned half = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
-          for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(half, sum, d);
-          if ((p & (kLanes - 1)) == 0)
-            neg_sum[((half_blk * 128 + 8 * p) >> GS) * 8 * NT + m] = sum * (-8.0f / 16777216.0f);
-          if (p == 0) x_scale[half_blk * 8 * NT + m] = e == 128 ? 4096.0f : pow2i(e - 2);
+            for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
+            const int e = max(int(__float_as_uint(amax) >> 23) - 127, -113);
+            const float f = e == 128 ? 1.0f : pow2i(14 - e);
+            uint4 v;
+            v.x = pack_f16(x[0] * f, x[4] * f);
+            v.y = pack_f16(x[1] * f * 0.0625f, x[5] * f * 0.0625f);
+            v.z = pack_f16(x[2] * f, x[6] * f);
+            v.w = pack_f16(x[3] * f * 0.0625f, x[7] * f * 0.0625f);
+            // odd tokens have the halves of 128 bytes exchanged: 8 tokens' pieces lie in different banks
+            xs[m * L.x_row + ((16 * half_blk + p) ^ ((m & 1) << 2))] = v;
+            float sum = f16_sum(v.x) + f16_sum(v.z) + 16.0f * (f16_sum(v.y) + f16_sum(v.w));
+            constexpr int kLanes = 1 << (GS - 3);  // of a group
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(half, sum, d);
+            if ((p & (kLanes - 1)) == 0)
+              neg_sum[((half_blk * 128 + 8 * p) >> GS) * 8 * NT + m] = sum * (-8.0f / 16777216.0f);
+            if (p == 0) x_scale[half_blk * 8 * NT + m] = e == 128 ? 4096.0f : pow2i(e - 2);
+          }
         }
         __syncthreads();
       }
 
-      for (int i = 0; i < P.chunk && chunk0 + i < groups; ++i) {
+      const int n_here = min(P.chunk, groups - chunk0);
+      for (int i = 0; i < n_here; ++i) {
         const int row0 = 16 * (tile0 + (chunk0 + i) * 2);
         float y[MT][NT][4];
 #pragma unroll
@@ -366,16 +391,14 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
             for (int c4 = 0; c4 < 4; ++c4) {
               const int c = 4 * hb + c4;
               uint4 x[NT];
+              float neg[NT][4];
 #pragma unroll
               for (int u = 0; u < NT; ++u) {
-                lds128_if(has_x[u], x_lane[u] + (blk * 8 + c) * 64, x[u]);
+                lds128_if(has_x[u], x_lane[u][c & 1] + (blk * 8 + c) * 64, x[u]);
                 if (c4 % kPer == 0) {
-                  const float2 neg = *reinterpret_cast<const float2*>(neg_sum + ((blk * 8 + c) / kPer * NT + u) * 8 + 2 * q);
-#pragma unroll
-                  for (int t = 0; t < MT; ++t) {
-                    acc[t][u][0] = acc[t][u][2] = neg.x;
-                    acc[t][u][1] = acc[t][u][3] = neg.y;
-                  }
+                  const float2 v = *reinterpret_cast<const float2*>(neg_sum + ((blk * 8 + c) / kPer * NT + u) * 8 + 2 * q);
+                  neg[u][0] = neg[u][2] = v.x;
+                  neg[u][1] = neg[u][3] = v.y;
                 }
               }
 #pragma unroll
@@ -385,8 +408,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
                 const uint32_t r0 = a0 >> 8, r1 = a1 >> 8;
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
-                  mma(acc[t][u], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u, a1 & 0x00F000F0u, x[u].x, x[u].y);
-                  mma(acc[t][u], r0 & 0x000F000Fu, r1 & 0x000F000Fu, r0 & 0x00F000F0u, r1 & 0x00F000F0u, x[u].z, x[u].w);
+                  mma(acc[t][u], a0 & 0x000F000Fu, a1 & 0x000F000Fu, a0 & 0x00F000F0u, a1 & 0x00F000F0u, x[u].x, x[u].y,
+                      c4 % kPer == 0 ? neg[u] : acc[t][u]);
+                  mma(acc[t][u], r0 & 0x000F000Fu, r1 & 0x000F000Fu, r0 & 0x00F000F0u, r1 & 0x00F000F0u, x[u].z, x[u].w,
+                      acc[t][u]);
                 }
                 if (c4 % kPer == kPer - 1) {
                   const int g = c / kPer;
@@ -427,18 +452,25 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
                 reduce[kw * outs + m * kGroupRows + 16 * (rw + t) + n + 8 * (k >> 1)] = y[t][u][k];
           }
         __syncthreads();
-        for (int o = threadIdx.x; o < outs; o += C::kThreads) {
+        const int o = threadIdx.x;  // outs <= threads
+        if (o < outs) {
           float v = 0.0f;
 #pragma unroll
           for (int w = 0; w < kKWarps; ++w) v += reduce[w * outs + o];
-          if (slices) {
-            if (b0 > 0) v += kept[i * outs + o];
-            kept[i * outs + o] = v;
-          }
+          if (b0 > 0) v += kept[0];
+#pragma unroll
+          for (int j = 0; j + 1 < kKept; ++j) kept[j] = kept[j + 1];  // with slices, a chunk is kKept groups at most:
+          kept[kKept - 1] = v;                                       // the next slice finds this one's sum first
           const int row = row0 + o % kGroupRows;
           if (b0 + nb == P.blocks && row < P.N && row < 16 * tile1)
             store_y(static_cast<uint16_t*>(P.Y) + int64_t(o / kGroupRows) * P.N + row, v * 4096.0f, P.dtype);
         }
+      }
+      for (int i = n_here; i < kKept; ++i) {  // turn a shorter chunk's sums round as well
+        const float v = kept[0];
+#pragma unroll
+        for (int j = 0; j + 1 < kKept; ++j) kept[j] = kept[j + 1];
+        kept[kKept - 1] = v;
       }
     }
   }
@@ -455,11 +487,11 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   const int grid = P.tiles < C::kCtas * num_sms ? P.tiles : C::kCtas * num_sms;
   const int per_cta = ((P.tiles + grid - 1) / grid + 1) / 2;
   // a slice: whole rounds of the warps, as many as fit
-  const int fit = (C::kXBytes / P.M - 64) / (kBlockK * 2) / kKWarps * kKWarps;
+  const int fit = C::kXBytes / P.M / (kBlockK * 2) / kKWarps * kKWarps;
   const bool slices = P.blocks > fit;
   P.slice_blocks = slices ? fit : P.blocks;
-  P.chunk = slices && per_cta > C::kKept ? C::kKept : per_cta;
-  const Layout L = layout<NT, GS>(P.M, P.slice_blocks, P.chunk, slices);
+  P.chunk = slices && per_cta > kKept ? kKept : per_cta;
+  const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   auto kernel = gemm4_kernel<S, NT, GS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
   if (e != cudaSuccess) return e;
