@@ -99,8 +99,6 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // warps for either tile, one CTA per SM.  K beyond what X's place holds is taken
 // in slices, the sums of four row groups kept meanwhile by the threads that add them.
 //
-// After the bytes, shared-memory passes bound it: an operand of X (16 bytes a
-// lane) costs a pass per 8 lanes; lanes of tokens beyond M load nothing.
 namespace g4 {
 
 constexpr int kBlockK = 256, kBoxBytes = 16 * 128;
@@ -151,23 +149,10 @@ __host__ __device__ inline Layout layout(int M, int slice_blocks) {
 __device__ __forceinline__ void store_y(uint16_t* at, float v, int dtype) {
   *at = dtype == PATCH_DTYPE_BF16 ? f32_to_bf16_rne(v) : __half_as_ushort(__float2half_rn(v));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-// where `on` is false v holds anything: a token beyond M, whose column is not stored
-__device__ __forceinline__ void lds128_if(bool on, uint32_t a, uint4& v) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "r"(a), "r"(uint32_t(on)));
-}
 // d = a b + c
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1, const float (&c)[4]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
@@ -252,7 +237,6 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
     fet.boxes = max(min(MT, tile1 - fet.tile), 0);  // a last group may have one tile only: the other's sums are not stored
     fet.src = static_cast<const S*>(P.scales) + int64_t(min(16 * fet.tile + lane, P.N - 1)) * row_groups + fet.b0 * kGroups;
   };
-  const uint32_t ring = tc::smem_u32(smem) + warp * kStages * C::kStageBytes;
   settle(false);
   int issued = 0, done = 0;
   auto fetch = [&]() {  // the whole warp; one group of asynchronous copies a call, on every lane
@@ -288,17 +272,15 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   };
   for (int s = 0; s < kStages; ++s) fetch();
 
-  uint32_t x_lane[NT][2];  // of even and odd chunks
-  bool has_x[NT];
+  const uint4* x_lane[NT][2];  // of even and odd chunks; tokens beyond M read the last one's, their columns are not stored
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    has_x[t] = 8 * t + n < P.M;
     const int m = min(8 * t + n, P.M - 1);
-    x_lane[t][0] = tc::smem_u32(xs) + uint32_t(m * L.x_row + q) * 16 + (m & 1) * 64;
-    x_lane[t][1] = x_lane[t][0] - (m & 1) * 128;
+    x_lane[t][0] = xs + m * L.x_row + q + (m & 1) * 4;
+    x_lane[t][1] = x_lane[t][0] - (m & 1) * 8;
   }
   // the lane's words: row n, chunk c of 16 bytes at c ^ n (128-byte swizzle); row n + 8 is 1024 bytes on
-  const uint32_t word0 = ring + n * 128 + n * 16 + 4 * q;
+  const uint32_t word0 = n * 128 + n * 16 + 4 * q;
 
   float kept[kKept] = {};
   for (int chunk0 = 0; chunk0 < groups; chunk0 += P.chunk) {
@@ -382,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
               if constexpr (kScaleRow == 8) *reinterpret_cast<uint2*>(sc[t][h]) = *reinterpret_cast<const uint2*>(at);
               if constexpr (kScaleRow == 4) *reinterpret_cast<uint32_t*>(sc[t][h]) = *reinterpret_cast<const uint32_t*>(at);
             }
-          const uint32_t words = word0 + st * C::kStageBytes;
+          const uint8_t* words = smem + (warp * kStages + st) * C::kStageBytes;
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {  // 128 k
             constexpr int kPer = 1 << (GS - 5);  // chunks of 32 k in a group
@@ -394,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
               float neg[NT][4];
 #pragma unroll
               for (int u = 0; u < NT; ++u) {
-                lds128_if(has_x[u], x_lane[u][c & 1] + (blk * 8 + c) * 64, x[u]);
+                x[u] = x_lane[u][c & 1][(blk * 8 + c) * 4];
                 if (c4 % kPer == 0) {
                   const float2 v = *reinterpret_cast<const float2*>(neg_sum + ((blk * 8 + c) / kPer * NT + u) * 8 + 2 * q);
                   neg[u][0] = neg[u][2] = v.x;
@@ -403,8 +385,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
               }
 #pragma unroll
               for (int t = 0; t < MT; ++t) {
-                const uint32_t at = (words ^ (c << 4)) + t * kBoxBytes;
-                const uint32_t a0 = lds32(at), a1 = lds32(at + 1024);
+                const uint8_t* at = words + (word0 ^ (c << 4)) + t * kBoxBytes;
+                const uint32_t a0 = *reinterpret_cast<const uint32_t*>(at), a1 = *reinterpret_cast<const uint32_t*>(at + 1024);
                 const uint32_t r0 = a0 >> 8, r1 = a1 >> 8;
 #pragma unroll
                 for (int u = 0; u < NT; ++u) {
