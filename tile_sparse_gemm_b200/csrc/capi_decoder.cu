@@ -161,7 +161,7 @@ patch_status_t patch_kv8_append(const patch_heads* k, const patch_heads* v, int6
   P.kv_heads = int(cache->kv_heads);
   P.page = int(cache->page);
   P.rot_units = table ? int(rot_dim / 16) : 0;
-  return launch_kv8_append(P, int(cache->head_dim), dtype, layout, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_kv8_append(P, int(cache->head_dim), dtype, layout, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PATCH_OK
              : PATCH_ERR_CUDA;
 }

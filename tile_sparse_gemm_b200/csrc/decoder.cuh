@@ -30,14 +30,14 @@ struct RopeParams {
   const float* table;
   int32_t* status;
   int64_t n_pos;
-  int rot_units, units;                  // units of a head: rotated ones first
-  int heads_per_pass, heads_per_thread;  // set by the launcher
+  int rot_units, units;  // units of a head: rotated ones first
+  int heads_per_pass;    // set by the launcher
   float sign;                            // of the sines
 };
 
 cudaError_t launch_rope_table(int64_t n_pos, int half, const RopeTableParams& P, float* table, int num_sms,
                               cudaStream_t stream);
-cudaError_t launch_rope(RopeParams P, int64_t n_tokens, int dtype, int layout, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& P, int64_t n_tokens, int dtype, int layout, int num_sms, cudaStream_t stream);
 
 struct AppendParams {
   const void* x[2];  // k, v
@@ -49,8 +49,9 @@ struct AppendParams {
   int32_t* status;
   int64_t n_pages, max_pages, n_pos;
   int n_tokens, batch, kv_heads, page, rot_units;
+  int heads_per_cta;  // set by the launcher
 };
-cudaError_t launch_kv8_append(const AppendParams& P, int head_dim, int dtype, int layout, cudaStream_t stream);
+cudaError_t launch_kv8_append(AppendParams P, int head_dim, int dtype, int layout, int num_sms, cudaStream_t stream);
 
 struct AttnParams {
   const void* q;

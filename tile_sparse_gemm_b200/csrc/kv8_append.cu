@@ -1,12 +1,17 @@
 // New keys and values into the paged 8-bit cache, keys rotated on the way
 // (include/patch.h: patch_kv8_append).
 //
-// One CTA per touched page, head and tensor (k or v): its new tokens stay in
-// registers (fp32) between the pass that finds their largest magnitude and the
-// one that rounds them, so each input is read once and each output written
-// once.  The scale is a power of two: e4m3 keeps its relative precision under
-// any scale, scaling is exact, and a page whose scale grows as tokens arrive is
-// stored again without a second rounding.
+// A page, head and tensor (k or v) belongs to one CTA, which finds its new tokens'
+// largest magnitude, takes the scale and rounds them.  The scale is a power of
+// two: e4m3 keeps its relative precision under any scale, scaling is exact, and a
+// page whose scale grows as tokens arrive is stored again without a second rounding.
+//
+// Prompts are bound by bandwidth (2 bytes in, 1 out): a thread holds one unit of 16
+// elements of a page in registers between the two passes, each input is read once
+// and each output written once; the CTA takes several heads, the next one's loads
+// under way meanwhile, and reads the angles of the page's tokens once for all of
+// them.  Decode steps (a token or a few per page) are bound by latency: small CTAs,
+// one head each, that read their few tokens twice.
 #include "common.cuh"
 #include "decoder.cuh"
 #include "kernels.cuh"
@@ -34,138 +39,231 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
   return __half2float(__half(h));
 }
 
-// kUnits units of 16 elements per thread: a rotated unit is 8 pairs (two
-// 8-element pieces), one behind the rotated part 16 elements in a row.
-template <typename T, int D, bool kInterleaved, int kThreads, int kUnits>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_constant__ AppendParams P) {
-  constexpr int kPerToken = D / 16;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // Item -> (sequence, page of it).  Sequence b owns the items from
-  // cu[b] / page + 2 b on: at least as many as the pages its tokens touch.
-  const int64_t item = blockIdx.x;
-  int b, j;
-  int64_t row0, n;
+// A touched page: the tokens begin .. begin + count - 1 of a sequence are rows row .. of k and v.
+struct Touched {
+  int64_t row, begin, phys;
+  int off, count;
+};
+
+// Item -> (sequence, page of it).  Sequence b owns the items from cu[b] / page + 2 b
+// on: at least as many as the pages its tokens touch.  count == 0: none.
+__device__ __forceinline__ Touched touched(const AppendParams& P, int64_t item) {
+  Touched t = {};
+  int b, j = 0;
+  int64_t row0, n = 1;
   if (P.cu_new) {
     const int32_t* cu = P.cu_new;
     const int page = P.page;
-    b = warp_find(P.batch, item, [&](int i) { return int64_t(cu[i]) / page + 2 * i; });
-    if (b >= P.batch) return;
+    b = warp_find(P.batch, item, [&](int i) { return int64_t(cu[i] / page) + 2 * i; });
+    if (b >= P.batch) return t;
     row0 = cu[b];
     n = min(int64_t(cu[b + 1]), int64_t(P.n_tokens)) - row0;
-    if (row0 < 0) return;
+    if (row0 < 0) return t;
     j = int(item - (row0 / page + 2 * b));
   } else {
     b = int(item);
-    j = 0;
     row0 = b;
-    n = 1;
   }
-  const int64_t past = P.past_lens[b];
-  const int64_t page_no = past / P.page + j;
-  const int64_t begin = max(past, page_no * P.page), end = min(past + n, (page_no + 1) * P.page);
-  if (begin >= end) return;
-  const int h = blockIdx.y, which = blockIdx.z;
-  const int64_t phys = past >= 0 && page_no < P.max_pages ? P.block_table[b * P.max_pages + page_no] : -1;
-  const bool turn = which == 0 && P.rot_units > 0;
-  if (phys < 0 || phys >= P.n_pages || (turn && end > P.n_pos)) {
-    if (threadIdx.x == 0) set_status(P.status, PATCH_DEV_BOUNDS);
-    return;
-  }
-  const int off = int(begin - page_no * P.page), count = int(end - begin);
-  const T* src = static_cast<const T*>(P.x[which]) + (row0 + begin - past) * P.ts[which] + h * P.hs[which];
+  const int past = P.past_lens[b];
+  const int64_t page_no = max(past, 0) / P.page + j;
+  const int64_t begin = max(int64_t(past), page_no * P.page), end = min(past + n, (page_no + 1) * P.page);
+  if (begin >= end) return t;
+  t.begin = begin;
+  t.count = int(end - begin);
+  t.off = int(begin - page_no * P.page);
+  t.row = row0 + begin - past;
+  t.phys = past >= 0 && page_no < P.max_pages ? P.block_table[b * P.max_pages + page_no] : -1;
+  return t;
+}
 
-  float x[kUnits][16];
-  uint32_t amax = 0;
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int idx = u * kThreads + threadIdx.x, tok = idx / kPerToken, unit = idx % kPerToken;
-    if (tok >= count) continue;
-    const T* row = src + tok * P.ts[which];
-    const bool pair = turn && unit < P.rot_units;
-    const int d0 = pair && !kInterleaved ? 8 * unit : 16 * unit;
-    const int d1 = pair && !kInterleaved ? d0 + 8 * P.rot_units : d0 + 8;
-    load16(row + d0, x[u]);
-    load16(row + d1, x[u] + 8);
-    if (pair) {
-      float cs[16];
-      const float4* tab =
-          reinterpret_cast<const float4*>(P.table + (begin + tok) * (16 * P.rot_units) + 16 * unit);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(cs + 4 * i) = __ldg(tab + i);
-      rotate_unit<8, kInterleaved>(x[u], cs, 1.0f);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t m = __float_as_uint(x[u][i]) & 0x7FFFFFFFu;
-      if (m < 0x7F800000u) amax = max(amax, m);  // infinities and NaN do not set the scale
-    }
+// Where a unit of 16 elements lies in a head: a rotated unit is 8 pairs (two
+// 8-element pieces), one behind the rotated part 16 elements in a row.
+template <bool kInterleaved>
+struct Unit {
+  int tok, unit, d0, d1;
+  bool pair;
+  __device__ __forceinline__ Unit(int idx, int per_token, bool turn, int rot_units) {
+    tok = idx / per_token;
+    unit = idx % per_token;
+    pair = turn && unit < rot_units;
+    d0 = pair && !kInterleaved ? 8 * unit : 16 * unit;
+    d1 = pair && !kInterleaved ? d0 + 8 * rot_units : d0 + 8;
   }
-  // largest magnitude over the CTA
-  __shared__ uint32_t part[kThreads / 32];
-  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __device__ __forceinline__ void angles(const AppendParams& P, int64_t begin, float (&cs)[16]) const {
+    const float4* tab = reinterpret_cast<const float4*>(P.table + (begin + tok) * (16 * P.rot_units) + 16 * unit);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(cs + 4 * i) = __ldg(tab + i);
+  }
+};
+
+// bits of the largest finite magnitude: infinities and NaN do not set the scale
+__device__ __forceinline__ uint32_t magnitude(const float (&x)[16], uint32_t amax) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    if (m < 0x7F800000u) amax = max(amax, m);
+  }
+  return amax;
+}
+
+__device__ __forceinline__ void store_unit(uint8_t* row, int d0, int d1, const float (&x)[16], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = pack_e4m3x4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+  *reinterpret_cast<uint2*>(row + d0) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(row + d1) = make_uint2(w[2], w[3]);
+}
+
+// the CTA's largest value, on every thread (one barrier)
+template <int kThreads>
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* part) {
+  v = __reduce_max_sync(0xFFFFFFFFu, v);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) amax = max(amax, part[i]);
-  float* scale_at = P.scale[which] + phys * P.kv_heads + h;
-  float scale = pow2i(scale_exponent(amax));
-  const float held = off > 0 ? *scale_at : 0.0f;
-  scale = fmaxf(scale, held);
-  const float inv = 1.0f / scale;  // exact: a power of two
-  __syncthreads();                 // everyone has read the old scale
-  if (threadIdx.x == 0) *scale_at = scale;
+  const int lane = threadIdx.x & 31;
+  return __reduce_max_sync(0xFFFFFFFFu, lane < kThreads / 32 ? part[lane] : 0u);
+}
 
-  uint8_t* dst = P.cache[which] + (phys * P.kv_heads + h) * (int64_t(P.page) * D);
-  if (off > 0 && scale > held) {  // store the tokens the page holds again
-    const float f = held * inv;
+// The page's scale, given the new tokens' largest magnitude and (off > 0) its present one; the
+// tokens that the page holds are stored again if it grows.
+template <int D, int kThreads>
+__device__ __forceinline__ float settle_scale(uint32_t amax, float held, int off, float* scale_at, uint8_t* page) {
+  const float scale = fmaxf(pow2i(scale_exponent(amax)), held);
+  if (threadIdx.x == 0) *scale_at = scale;
+  if (off > 0 && scale > held) {
+    const float f = held / scale;  // exact: powers of two
     for (int i = threadIdx.x; i < off * (D / 16); i += kThreads) {
-      uint4 w = reinterpret_cast<uint4*>(dst)[i];
+      uint4 w = reinterpret_cast<uint4*>(page)[i];
       uint32_t* e = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         e[q] = pack_e4m3x4(e4m3_to_f32(e[q] & 255) * f, e4m3_to_f32((e[q] >> 8) & 255) * f,
                            e4m3_to_f32((e[q] >> 16) & 255) * f, e4m3_to_f32(e[q] >> 24) * f);
-      reinterpret_cast<uint4*>(dst)[i] = w;
+      reinterpret_cast<uint4*>(page)[i] = w;
     }
   }
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int idx = u * kThreads + threadIdx.x, tok = idx / kPerToken, unit = idx % kPerToken;
-    if (tok >= count) continue;
-    const bool pair = turn && unit < P.rot_units;
-    const int d0 = pair && !kInterleaved ? 8 * unit : 16 * unit;
-    const int d1 = pair && !kInterleaved ? d0 + 8 * P.rot_units : d0 + 8;
-    uint8_t* row = dst + (off + tok) * D;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = pack_e4m3x4(x[u][4 * i] * inv, x[u][4 * i + 1] * inv, x[u][4 * i + 2] * inv, x[u][4 * i + 3] * inv);
-    *reinterpret_cast<uint2*>(row + d0) = make_uint2(w[0], w[1]);
-    *reinterpret_cast<uint2*>(row + d1) = make_uint2(w[2], w[3]);
+  return scale;
+}
+
+// kThreads = page * D / 16: one unit of a full page each.
+template <typename T, int D, bool kInterleaved, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv8_append_kernel(const __grid_constant__ AppendParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Touched t = touched(P, blockIdx.x);
+  if (t.count == 0) return;
+  const int which = blockIdx.z;
+  const bool turn = which == 0 && P.rot_units > 0;
+  const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(h0 + P.heads_per_cta, P.kv_heads);
+  const Unit<kInterleaved> u(threadIdx.x, D / 16, turn, P.rot_units);
+  const bool live = u.tok < t.count;
+  const T* src = static_cast<const T*>(P.x[which]) + (t.row + u.tok) * P.ts[which] + h0 * P.hs[which];
+  uint4 raw0 = {}, raw1 = {};
+  if (live) {
+    raw0 = *reinterpret_cast<const uint4*>(src + u.d0);
+    raw1 = *reinterpret_cast<const uint4*>(src + u.d1);
+  }
+  if (t.phys < 0 || t.phys >= P.n_pages || (turn && t.begin + t.count > P.n_pos)) {
+    if (threadIdx.x == 0) set_status(P.status, PATCH_DEV_BOUNDS);
+    return;
+  }
+  float cs[16];
+  if (u.pair && live) u.angles(P, t.begin, cs);
+  __shared__ uint32_t part[2][kThreads / 32];
+  for (int h = h0; h < h1; ++h) {
+    float x[16];
+    load16(reinterpret_cast<const T*>(&raw0), x);
+    load16(reinterpret_cast<const T*>(&raw1), x + 8);
+    if (u.pair && live) rotate_unit<8, kInterleaved>(x, cs, 1.0f);
+    if (h + 1 < h1 && live) {
+      src += P.hs[which];
+      raw0 = *reinterpret_cast<const uint4*>(src + u.d0);
+      raw1 = *reinterpret_cast<const uint4*>(src + u.d1);
+    }
+    float* scale_at = P.scale[which] + t.phys * P.kv_heads + h;
+    const float held = t.off > 0 ? *scale_at : 0.0f;
+    // two buffers in turn: a thread is at most one barrier ahead
+    const uint32_t amax = cta_max<kThreads>(magnitude(x, 0), part[h & 1]);
+    uint8_t* page = P.cache[which] + (t.phys * P.kv_heads + h) * (int64_t(P.page) * D);
+    const float scale = settle_scale<D, kThreads>(amax, held, t.off, scale_at, page);
+    if (live) store_unit(page + (t.off + u.tok) * D, u.d0, u.d1, x, 1.0f / scale);
+  }
+}
+
+// Any number of tokens with few threads: a unit is read again for the second pass.
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(64) kv8_append_few_kernel(const __grid_constant__ AppendParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Touched t = touched(P, blockIdx.x);
+  if (t.count == 0) return;
+  const int which = blockIdx.z, h = blockIdx.y;
+  const bool turn = which == 0 && P.rot_units > 0;
+  const T* src = static_cast<const T*>(P.x[which]) + t.row * P.ts[which] + h * P.hs[which];
+  if (t.phys < 0 || t.phys >= P.n_pages || (turn && t.begin + t.count > P.n_pos)) {
+    if (threadIdx.x == 0) set_status(P.status, PATCH_DEV_BOUNDS);
+    return;
+  }
+  auto load = [&](const Unit<kInterleaved>& u, float (&x)[16]) {
+    const T* row = src + u.tok * P.ts[which];
+    load16(row + u.d0, x);
+    load16(row + u.d1, x + 8);
+    if (u.pair) {
+      float cs[16];
+      u.angles(P, t.begin, cs);
+      rotate_unit<8, kInterleaved>(x, cs, 1.0f);
+    }
+  };
+  float* scale_at = P.scale[which] + t.phys * P.kv_heads + h;
+  const float held = t.off > 0 ? *scale_at : 0.0f;
+  const int units = t.count * (D / 16);
+  uint32_t amax = 0;
+  for (int i = threadIdx.x; i < units; i += 64) {
+    float x[16];
+    load(Unit<kInterleaved>(i, D / 16, turn, P.rot_units), x);
+    amax = magnitude(x, amax);
+  }
+  __shared__ uint32_t part[2];
+  amax = cta_max<64>(amax, part);
+  uint8_t* page = P.cache[which] + (t.phys * P.kv_heads + h) * (int64_t(P.page) * D);
+  const float scale = settle_scale<D, 64>(amax, held, t.off, scale_at, page);
+  for (int i = threadIdx.x; i < units; i += 64) {
+    const Unit<kInterleaved> u(i, D / 16, turn, P.rot_units);
+    float x[16];
+    load(u, x);
+    store_unit(page + (t.off + u.tok) * D, u.d0, u.d1, x, 1.0f / scale);
   }
 }
 
 template <typename T, int D, bool kInterleaved>
-static cudaError_t launch_append(const AppendParams& P, cudaStream_t stream) {
+static cudaError_t launch_append(AppendParams P, int num_sms, cudaStream_t stream) {
   const int64_t items = P.cu_new ? P.n_tokens / P.page + 2 * int64_t(P.batch) : P.batch;
-  const dim3 grid(unsigned(items), unsigned(P.kv_heads), 2);
+  // Less than a quarter of a page per sequence: the small CTAs (64 sequences of one token, 8 heads:
+  // FEW_US us against FEW_OTHER).
+  if (int64_t(P.n_tokens) * 4 < int64_t(P.batch) * P.page)
+    return launch_pdl(kv8_append_few_kernel<T, D, kInterleaved>, dim3(unsigned(items), unsigned(P.kv_heads), 2),
+                      dim3(64), 0, stream, P);
+  // Several heads a CTA as long as every SM still has some.
+  const int64_t ctas = (P.n_tokens / P.page + 1) * P.kv_heads * 2;
+  P.heads_per_cta = int(ctas / (8 * int64_t(num_sms)));
+  P.heads_per_cta = P.heads_per_cta < 1 ? 1 : P.heads_per_cta > 8 ? 8 : P.heads_per_cta;
+  const dim3 grid(unsigned(items), unsigned((P.kv_heads + P.heads_per_cta - 1) / P.heads_per_cta), 2);
   const int units = P.page * (D / 16);  // of a full page: 64 ... 1024
-  if (units <= 64) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 64, 1>, grid, dim3(64), 0, stream, P);
-  if (units <= 128) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 128, 1>, grid, dim3(128), 0, stream, P);
-  if (units <= 256) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 256, 1>, grid, dim3(256), 0, stream, P);
-  if (units <= 512) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 256, 2>, grid, dim3(256), 0, stream, P);
-  return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 256, 4>, grid, dim3(256), 0, stream, P);
+  if (units == 64) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 64>, grid, dim3(64), 0, stream, P);
+  if (units == 128) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 128>, grid, dim3(128), 0, stream, P);
+  if (units == 256) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 256>, grid, dim3(256), 0, stream, P);
+  if (units == 512) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 512>, grid, dim3(512), 0, stream, P);
+  return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 1024>, grid, dim3(1024), 0, stream, P);
 }
 
-cudaError_t launch_kv8_append(const AppendParams& P, int head_dim, int dtype, int layout, cudaStream_t stream) {
+cudaError_t launch_kv8_append(AppendParams P, int head_dim, int dtype, int layout, int num_sms, cudaStream_t stream) {
   const bool il = layout == PATCH_ROPE_INTERLEAVED && P.rot_units > 0;
   if (dtype == PATCH_DTYPE_BF16) {
     if (head_dim == 128)
-      return il ? launch_append<__nv_bfloat16, 128, true>(P, stream) : launch_append<__nv_bfloat16, 128, false>(P, stream);
-    return il ? launch_append<__nv_bfloat16, 64, true>(P, stream) : launch_append<__nv_bfloat16, 64, false>(P, stream);
+      return il ? launch_append<__nv_bfloat16, 128, true>(P, num_sms, stream) : launch_append<__nv_bfloat16, 128, false>(P, num_sms, stream);
+    return il ? launch_append<__nv_bfloat16, 64, true>(P, num_sms, stream) : launch_append<__nv_bfloat16, 64, false>(P, num_sms, stream);
   }
-  if (head_dim == 128) return il ? launch_append<__half, 128, true>(P, stream) : launch_append<__half, 128, false>(P, stream);
-  return il ? launch_append<__half, 64, true>(P, stream) : launch_append<__half, 64, false>(P, stream);
+  if (head_dim == 128) return il ? launch_append<__half, 128, true>(P, num_sms, stream) : launch_append<__half, 128, false>(P, num_sms, stream);
+  return il ? launch_append<__half, 64, true>(P, num_sms, stream) : launch_append<__half, 64, false>(P, num_sms, stream);
 }
 
 }  // namespace patch

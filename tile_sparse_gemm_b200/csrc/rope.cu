@@ -48,10 +48,13 @@ cudaError_t launch_rope_table(int64_t n_pos, int half, const RopeTableParams& P,
   return cudaGetLastError();
 }
 
-// A unit is one thread's work on one head: V pairs (two 16-byte pieces, V = 8
-// elements of 16 bits or 4 of 32 each) inside the rotated part, one 16-byte
-// piece behind it.
-template <typename T, bool kInterleaved>
+// Bandwidth-bound: each element is read and written once, but a token's row of
+// the table (64 bytes per 32 bytes of a head) would pass through L1 again for
+// every head.  A unit is one thread's work on one head: V pairs (two 16-byte
+// pieces, V = 8 elements of 16 bits or 4 of 32 each) inside the rotated part, one
+// 16-byte piece behind it.  A thread keeps its unit's V angles in registers and
+// takes kHeads heads with them, their loads under way together.
+template <typename T, bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams P) {
   constexpr int V = 16 / sizeof(T);
   const int64_t t = blockIdx.x;
@@ -63,6 +66,25 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
     return;
   }
   const bool rotated = unit < P.rot_units;
+  // element offsets of the unit's pieces
+  const int d0 = !rotated ? 2 * V * P.rot_units + V * (unit - P.rot_units) : kInterleaved ? 2 * V * unit : V * unit;
+  const int d1 = kInterleaved ? d0 + V : d0 + V * P.rot_units;
+  const T* src[kHeads];
+  T* dst[kHeads];
+  uint4 x0[kHeads], x1[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int head = (blockIdx.y * kHeads + i) * P.heads_per_pass + sub;
+    src[i] = nullptr;
+    if (head >= P.q.heads + P.k.heads) continue;
+    const bool is_k = head >= P.q.heads;
+    const RopeHeads& H = is_k ? P.k : P.q;
+    const int h = is_k ? head - P.q.heads : head;
+    src[i] = static_cast<const T*>(H.src) + t * H.src_ts + h * H.src_hs;
+    dst[i] = static_cast<T*>(H.dst) + t * H.dst_ts + h * H.dst_hs;
+    x0[i] = *reinterpret_cast<const uint4*>(src[i] + d0);
+    if (rotated) x1[i] = *reinterpret_cast<const uint4*>(src[i] + d1);
+  }
   float cs[2 * V];
   if (rotated) {
     const float4* tab =
@@ -70,45 +92,44 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float4*>(cs + 4 * i) = __ldg(tab + i);
   }
-  // element offsets of the unit's pieces
-  const int d0 = !rotated ? 2 * V * P.rot_units + V * (unit - P.rot_units) : kInterleaved ? 2 * V * unit : V * unit;
-  const int d1 = kInterleaved ? d0 + V : d0 + V * P.rot_units;
-  for (int i = 0; i < P.heads_per_thread; ++i) {
-    int h = (blockIdx.y * P.heads_per_thread + i) * P.heads_per_pass + sub;
-    if (h >= P.q.heads + P.k.heads) break;
-    const bool is_k = h >= P.q.heads;
-    if (is_k) h -= P.q.heads;
-    const T* src = static_cast<const T*>(is_k ? P.k.src : P.q.src) + t * (is_k ? P.k.src_ts : P.q.src_ts) +
-                   h * (is_k ? P.k.src_hs : P.q.src_hs);
-    T* dst = static_cast<T*>(is_k ? P.k.dst : P.q.dst) + t * (is_k ? P.k.dst_ts : P.q.dst_ts) +
-             h * (is_k ? P.k.dst_hs : P.q.dst_hs);
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (!src[i]) continue;
     if (!rotated) {
-      if (src != dst) *reinterpret_cast<uint4*>(dst + d0) = *reinterpret_cast<const uint4*>(src + d0);
+      if (src[i] != dst[i]) *reinterpret_cast<uint4*>(dst[i] + d0) = x0[i];
       continue;
     }
     float x[2 * V];
-    load16(src + d0, x);
-    load16(src + d1, x + V);
+    load16(reinterpret_cast<const T*>(&x0[i]), x);
+    load16(reinterpret_cast<const T*>(&x1[i]), x + V);
     rotate_unit<V, kInterleaved>(x, cs, P.sign);
-    store16(dst + d0, x);
-    store16(dst + d1, x + V);
+    store16(dst[i] + d0, x);
+    store16(dst[i] + d1, x + V);
   }
 }
 
-cudaError_t launch_rope(RopeParams P, int64_t n_tokens, int dtype, int layout, int num_sms, cudaStream_t stream) {
+template <typename T>
+static cudaError_t launch_rope_type(RopeParams P, int64_t n_tokens, bool interleaved, int num_sms, cudaStream_t stream) {
   const int heads = P.q.heads + P.k.heads;
   P.heads_per_pass = P.units >= 128 ? 1 : 128 / P.units;
   if (P.heads_per_pass > heads) P.heads_per_pass = heads;
   const int passes = (heads + P.heads_per_pass - 1) / P.heads_per_pass;
-  P.heads_per_thread = 1;
-  const dim3 grid{unsigned(n_tokens), unsigned(passes)}, block{unsigned(P.heads_per_pass * P.units)};
+  const dim3 block{unsigned(P.heads_per_pass * P.units)};
+  // Four heads a thread (8192 tokens of 64 heads of 128: 59 us with one, 45 with four) where that still leaves
+  // several CTAs per SM, else one (16 tokens of 40 heads: 1.7 us).
+  if (passes > 1 && n_tokens * ((passes + 3) / 4) >= 4 * int64_t(num_sms)) {
+    const dim3 grid{unsigned(n_tokens), unsigned((passes + 3) / 4)};
+    return launch_pdl(interleaved ? rope_kernel<T, true, 4> : rope_kernel<T, false, 4>, grid, block, 0, stream, P);
+  }
+  const dim3 grid{unsigned(n_tokens), unsigned(passes)};
+  return launch_pdl(interleaved ? rope_kernel<T, true, 1> : rope_kernel<T, false, 1>, grid, block, 0, stream, P);
+}
+
+cudaError_t launch_rope(const RopeParams& P, int64_t n_tokens, int dtype, int layout, int num_sms, cudaStream_t stream) {
   const bool il = layout == PATCH_ROPE_INTERLEAVED;
-  if (dtype == PATCH_DTYPE_BF16)
-    return launch_pdl(il ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>, grid, block, 0,
-                      stream, P);
-  if (dtype == PATCH_DTYPE_FP16)
-    return launch_pdl(il ? rope_kernel<__half, true> : rope_kernel<__half, false>, grid, block, 0, stream, P);
-  return launch_pdl(il ? rope_kernel<float, true> : rope_kernel<float, false>, grid, block, 0, stream, P);
+  if (dtype == PATCH_DTYPE_BF16) return launch_rope_type<__nv_bfloat16>(P, n_tokens, il, num_sms, stream);
+  if (dtype == PATCH_DTYPE_FP16) return launch_rope_type<__half>(P, n_tokens, il, num_sms, stream);
+  return launch_rope_type<float>(P, n_tokens, il, num_sms, stream);
 }
 
 }  // namespace patch
