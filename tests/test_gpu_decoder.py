@@ -32,8 +32,9 @@ def i32(x):
 def within(got, want, bound, what=""):
     got = got.double()
     assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN elsewhere"
-    err = (got - want).abs().nan_to_num()
-    worst = float((err / bound).max()) if err.numel() else 0.0
+    held = ~want.isnan()  # a NaN is right where it is, and has no distance
+    err = ((got - want).abs() / bound)[held]
+    worst = float(err.max()) if err.numel() else 0.0
     assert worst <= 1.0, f"{what}: {worst:.3g} times the bound"
 
 
@@ -351,6 +352,23 @@ def test_attn_nan_reaches_only_the_rows_that_see_it():
         return q
     # 20 queries at positions 30 .. 49: token 40 is seen from position 40 on
     run_attn(2, 4, 2, 64, 16, [50, 60], [20, 2], BF16, seed=6, edit=edit)
+    # the same with 128-row tiles: 170 queries at positions 0 .. 169, a second NaN behind the first tile's last position
+    def more(q, cache, bt):
+        q = edit(q, cache, bt)
+        cache.v.view(torch.uint8)[int(bt[0, 9]), 1, 3, 63] = 0xFF
+        cache.k.view(torch.uint8)[int(bt[1, 8]), 1, 1, 2] = 0x7F  # a key: whole rows from position 129 on
+        return q
+    run_attn(2, 4, 2, 64, 16, [170, 150], [170, 150], BF16, seed=6, edit=more)
+
+
+@pytest.mark.parametrize("H,Hk,D,page,dtype", [(8, 2, 128, 64, BF16), (14, 2, 64, 16, FP16), (4, 4, 128, 32, FP16),
+                                               (16, 1, 64, 128, BF16)])
+@pytest.mark.parametrize("kv,q", [([64], [64]), ([5000], [130]), ([1, 700, 0, 2000], [300, 70, 90, 1999]),
+                                  ([256] * 40, [65 + i for i in range(40)])])
+def test_attn_prompts(H, Hk, D, page, dtype, kv, q):
+    """Many queries per sequence: tiles of 128 rows, whole ones and cut ones, ragged, some without keys."""
+    run_attn(len(kv), H, Hk, D, page, kv, q, dtype, seed=12, pad_rows=1)
+    run_attn(len(kv), H, Hk, D, page, kv, q, dtype, causal=False, seed=13, scale=-0.05)
 
 
 def test_attn_bad_lengths_and_pages_read_as_zeros():

@@ -21,7 +21,8 @@ LIB = PKG / "libpatch.so"
 LIB_DEBUG = PKG / "libpatch_debug.so"
 SOURCES = ["capi.cu", "hard_mask.cu", "pack.cu", "gemm_decode.cu", "gemm_decode_tc.cu", "gemm_prefill.cu",
            "gemm_decode_noalloc.cu", "gated_mlp.cu", "gemm_decode_chain.cu", "mma_probe.cu", "validate.cu",
-           "gemm64.cu", "capi_decoder.cu", "rope.cu", "kv8_append.cu", "attn_kv8.cu", "gemm4.cu"]
+           "gemm64.cu", "capi_decoder.cu", "rope.cu", "kv8_append.cu", "attn_kv8.cu",
+           "attn_kv8_rows.cu", "gemm4.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
 

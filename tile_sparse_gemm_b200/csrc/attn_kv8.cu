@@ -29,10 +29,7 @@
 // cache row serve directly as its operands, and values are transposed by a
 // byte permute of two tokens' words.  A page's key scale multiplies the scores,
 // its value scale (relative to the largest so far) the probabilities.
-#include "common.cuh"
-#include "decoder.cuh"
-#include "kernels.cuh"
-#include "tc_ptx.cuh"
+#include "attn_kv8.cuh"
 
 namespace patch {
 namespace attn {
@@ -40,7 +37,6 @@ namespace attn {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunkBytes = 4096;  // of keys, and of values
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
   CUtensorMap k_map, v_map;
@@ -75,129 +71,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// four e4m3 bytes to two fp16 pairs (exact)
-__device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ uint4 lds128(const uint8_t* a) { return *reinterpret_cast<const uint4*>(a); }
 __device__ __forceinline__ uint2 lds64(const uint8_t* a) { return *reinterpret_cast<const uint2*>(a); }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-
-// A row tile of one sequence and head: which tokens its rows see.
-struct Tile {
-  int b, h, rt;
-  int len, m, row0;    // the sequence's tokens, queries, first row of q
-  int chunk0, chunks;  // its run of chunks (at least one, so that every tile is written)
-  int hi;              // tokens from here on are seen by no row
-};
-
-__device__ __forceinline__ void sequence(const AttnParams& a, int b, int& len, int& m, int& row0) {
-  if (a.cu_q) {
-    row0 = min(max(a.cu_q[b], 0), a.n_tokens);
-    m = min(max(a.cu_q[b + 1], row0), a.n_tokens) - row0;
-  } else {
-    row0 = b;
-    m = 1;
-  }
-  len = int(min(int64_t(max(a.kv_lens[b], 0)), a.max_pages * a.page));
-}
-
-template <int CH, int R>
-__device__ __forceinline__ void set_rows(const AttnParams& a, int G, Tile& t) {
-  int hi = t.len, lo = 0;
-  if (a.causal) hi = max(0, min(t.len, t.len - t.m + min(t.m - 1, (t.rt * R + R - 1) / G) + 1));
-  if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + t.rt * R / G - a.window + 1));
-  t.hi = hi;
-  t.chunk0 = lo / CH;
-  t.chunks = max(1, (hi + CH - 1) / CH - t.chunk0);
-}
-template <int R>
-__device__ __forceinline__ int row_tiles(int m, int G) {
-  return (m * G + R - 1) / R;
-}
-
-// Shares are equal in units: a chunk is one, and a tile's own cost (its queries,
-// its output; about half a chunk's time in a warp) is kTileUnits in front of its chunks.
-constexpr int kTileUnits = 1;
-
-// units of all of a sequence's tiles of one head
-template <int CH, int R>
-__device__ __forceinline__ int64_t units_per_head(const AttnParams& a, int G, Tile& t) {
-  const int n = row_tiles<R>(t.m, G);
-  if (n == 0) return 0;
-  if (!a.causal) {
-    t.rt = 0;
-    set_rows<CH, R>(a, G, t);
-    return int64_t(n) * (t.chunks + kTileUnits);
-  }
-  int64_t s = 0;
-  for (t.rt = 0; t.rt < n; ++t.rt) {
-    set_rows<CH, R>(a, G, t);
-    s += t.chunks + kTileUnits;
-  }
-  return s;
-}
-// to the next tile, in the order (sequence, head, row tile)
-template <int CH, int R>
-__device__ __forceinline__ void next_tile(const AttnParams& a, int G, Tile& t) {
-  if (++t.rt >= row_tiles<R>(t.m, G)) {
-    t.rt = 0;
-    if (++t.h == a.kv_heads) {
-      t.h = 0;
-      do {
-        if (++t.b >= a.batch) return;
-        sequence(a, t.b, t.len, t.m, t.row0);
-      } while (t.m == 0);
-    }
-  }
-  set_rows<CH, R>(a, G, t);
-}
-
-// A warp's place in its share: chunks c .. c_end - 1 of tile t are next, `left`
-// units of the share count from the tile's first on.  c == c_end: done.
-struct Cursor {
-  Tile t;
-  int c, c_end;
-  int64_t left;
-
-  __device__ __forceinline__ void clip() { c_end = int(min(int64_t(t.chunks), max(left - kTileUnits, int64_t(0)))); }
-  template <int CH, int R>
-  __device__ __forceinline__ void next(const AttnParams& a, int G) {
-    left -= t.chunks + kTileUnits;
-    c = c_end = 0;
-    if (left <= kTileUnits) return;
-    next_tile<CH, R>(a, G, t);
-    clip();
-  }
-};
-
 // A piece of a tile that one warp did not do alone.
 struct Piece {
   int valid, ends;  // ends: it holds the tile's last chunk
@@ -206,10 +86,6 @@ struct Piece {
   int64_t pad2;
 };
 static_assert(sizeof(Piece) == 48, "kPieces");
-
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
-}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_constant__ Params P) {
@@ -222,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars) + warp * STAGES;
   float* scales = reinterpret_cast<float*>(smem + C::kScales) + warp * STAGES * 8;
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieces);
-  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // 8 sums, 8 x (sequence, units before it)
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 24 words
   int* abort_flag = reinterpret_cast<int*>(misc + 24);
   if (lane == 0) {
     for (int s = 0; s < STAGES; ++s) tc::mbar_init(bars + s, 1);
@@ -236,95 +112,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // queries, lengths and cache come from earlier kernels
 
-  // ---- this CTA's share of all units, [u0, u1) of W, and each warp's first sequence
-  auto units_of = [&](int b) -> int64_t {
-    if (b >= a.batch) return 0;
-    Tile t;
-    sequence(a, b, t.len, t.m, t.row0);
-    return units_per_head<CH, R>(a, G, t) * a.kv_heads;
-  };
-  auto warp_scan = [&](int64_t v) {  // inclusive
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v, d);
-      if (lane >= d) v += y;
-    }
-    return v;
-  };
-  const int64_t mine = units_of(threadIdx.x);  // the only sequences unless there are more than threads
-  int64_t rest = 0;
-  for (int b = threadIdx.x + kThreads; b < a.batch; b += kThreads) rest += units_of(b);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-      const int len = a.kv_lens[b];
-      if (len < 0 || len > a.max_pages * a.page) set_status(a.status, PATCH_DEV_BOUNDS);
-    }
-  int64_t in = warp_scan(mine), W = 0;
-  {
-    const int64_t all = a.batch > kThreads ? warp_scan(mine + rest) : in;
-    if (lane == 31) misc[warp] = all;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) W += misc[w];
-  }
-  const int64_t n_cta = min(int64_t(gridDim.x), W);
-  if (blockIdx.x >= n_cta) return;
-  // the first `more` CTAs take per + 1 units, the others per
-  const int64_t per = quotient(W, n_cta), more = W - per * n_cta;
-  const int64_t u0 = per * blockIdx.x + min(int64_t(blockIdx.x), more), u_n = per + (blockIdx.x < more ? 1 : 0);
-  auto owner = [&](int64_t u) {  // the CTA that a unit belongs to
-    const int64_t cut = more * (per + 1);
-    return u < cut ? quotient(u, per + 1) : more + quotient(u - cut, per);
-  };
-  int64_t before = 0;
-  for (int base = 0; base < a.batch; base += kThreads) {
-    const int64_t v = base ? units_of(base + threadIdx.x) : mine;
-    if (base || a.batch > kThreads) {
-      if (base) in = warp_scan(v);
-      __syncthreads();
-      if (lane == 31) misc[warp] = in;
-      __syncthreads();
-    }
-    int64_t ex = before + in - v;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) ex += misc[w];
-      before += misc[w];
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int64_t u = u0 + (u_n * w >> 3);
-      if (ex <= u && u < ex + v) {
-        misc[8 + 2 * w] = base + threadIdx.x;
-        misc[9 + 2 * w] = ex;
-      }
-    }
-    if (before >= u0 + u_n) break;
-  }
-  __syncthreads();
+  // ---- this CTA's share of all units, and each warp's first sequence
+  Share sh;
+  if (!make_share<CH, R, kWarps, kWarps>(a, G, misc, sh)) return;
 
   // ---- this warp's share
   Cursor cur;
-  {
-    const int64_t v0 = u0 + (u_n * warp >> 3), v1 = u0 + (u_n * (warp + 1) >> 3);
-    Tile& t = cur.t;
-    t.b = int(misc[8 + 2 * warp]);
-    sequence(a, t.b, t.len, t.m, t.row0);
-    int64_t off = v0 - misc[9 + 2 * warp];
-    const int64_t per_head = units_per_head<CH, R>(a, G, t);
-    t.h = int(quotient(off, per_head));
-    off -= per_head * t.h;
-    t.rt = 0;
-    set_rows<CH, R>(a, G, t);
-    while (off >= t.chunks + kTileUnits) {
-      off -= t.chunks + kTileUnits;
-      ++t.rt;
-      set_rows<CH, R>(a, G, t);
-    }
-    cur.left = v1 - (v0 - off);
-    cur.c = int(max(off - kTileUnits, int64_t(0)));
-    cur.clip();
-  }
+  cur.start<CH, R>(a, G, misc + kWarps + 2 * warp, sh.start(warp, kWarps), sh.start(warp + 1, kWarps));
 
   // ---- a second cursor runs ahead and fetches
   const uint32_t ring = tc::smem_u32(smem) + warp * C::kRingBytes;
@@ -681,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
 #pragma unroll
             for (int x = 0; x < 2; ++x) keep[((j * NT + nt) * 4 + 2 * x + e) * 32 + lane] = o[j][nt][2 * x + e];
         }
-      if (lane == 0) pieces[2 * warp + begins] = Piece{1, ends, t.row0, t.m, t.rt, t.h, t.chunks, 0, u0 + (u_n * (warp + 1) >> 3) - cur.left, 0};
+      if (lane == 0) pieces[2 * warp + begins] = Piece{1, ends, t.row0, t.m, t.rt, t.h, t.chunks, 0, sh.start(warp + 1, kWarps) - cur.left, 0};
     }
   }
   // after a timeout: let the copies in flight land before their memory is used again
@@ -729,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     } while (!ends && i < 2 * kWarps && !(pieces[i].valid && (i & 1)));
     bool write = true;
     if (comes_in || !ends) {  // cut between CTAs
-      const int64_t c0 = owner(first.unit0 + kTileUnits), c1 = owner(first.unit0 + kTileUnits + first.chunks - 1);
+      const int64_t c0 = sh.owner(first.unit0 + kTileUnits), c1 = sh.owner(first.unit0 + kTileUnits + first.chunks - 1);
       float* part = P.parts + (2 * blockIdx.x + (comes_in ? 0 : 1)) * int64_t(C::kStateFloats);
 #pragma unroll
       for (int k = 0; k < kEl; ++k) part[row * D + d0 + k] = x[k];
@@ -797,16 +591,25 @@ static cudaError_t launch(const Params& P, int num_sms, cudaStream_t stream) {
 
 }  // namespace attn
 
-// Counters first (one per CTA, left zero), then two tile states of up to 16 rows per CTA.
-static size_t attn_counter_bytes(int num_sms) { return (size_t(num_sms) * 4 + 255) / 256 * 256; }
+// Counters first (the same place for both kernels: up to two CTAs per SM, left zero), then two tile states per CTA.
+static size_t attn_counter_bytes(int num_sms) { return (size_t(num_sms) * 8 + 255) / 256 * 256; }
 
-size_t attn_kv8_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t head_dim, int num_sms) {
+// Tiles of 128 rows (attn_kv8_rows.cu) where a sequence and head have 64 query rows or more on average.
+static bool many_rows(int64_t n_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads) {
+  return n_tokens * (q_heads / kv_heads) >= 64 * batch;
+}
+
+size_t attn_kv8_workspace_bytes(int64_t n_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                int num_sms) {
+  if (many_rows(n_tokens, batch, q_heads, kv_heads)) return attn_kv8_rows_workspace_bytes(head_dim, num_sms);
   const size_t state = head_dim == 128 ? attn::Cfg<128, 2>::kStateBytes : attn::Cfg<64, 2>::kStateBytes;
   return attn_counter_bytes(num_sms) + 2 * size_t(num_sms) * state;
 }
 
-cudaError_t launch_attn_kv8(const AttnParams& a, int head_dim, int dtype, void* workspace, int num_sms,
-                            uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_attn_kv8(const AttnParams& a, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
+                            int num_sms, uint64_t limit_ns, cudaStream_t stream) {
+  if (many_rows(a.n_tokens, a.batch, a.heads, a.kv_heads))
+    return launch_attn_kv8_rows(a, head_dim, dtype, workspace, workspace_bytes, num_sms, limit_ns, stream);
   attn::Params P = {};
   P.a = a;
   P.counters = static_cast<uint32_t*>(workspace);

@@ -1,0 +1,622 @@
+// Attention over the paged 8-bit cache for sequences with many new tokens
+// (chunks of a prompt): tiles of 128 query rows on tcgen05 (include/patch.h:
+// patch_attn_kv8; attn_kv8.cu has the form for few rows and the mathematics).
+//
+// What bounds it: with 128 rows to a tile every cached byte meets 128 rows, so
+// it is bound by computing: two products of 128 x 64 x D a block of 64 tokens,
+// 8192 exponentials, and the conversion of the block to fp16.  Per SM that is
+// about 2 x 256 tensor-core cycles (D = 128), 512 cycles of exponentials and some
+// 700 of other softmax instructions, so the roles run side by side, and two CTAs
+// share an SM:
+//   warps 0-3   softmax, a thread per row: scores from tensor memory, the running
+//               maximum, probabilities as fp16 to shared memory.  The sum of the
+//               values stays in tensor memory and is rescaled only when a row's
+//               maximum grows by more than 2^8 (probabilities are at most 2^8 then,
+//               well inside fp16, and the sums are fp32);
+//   warps 4-7   convert the e4m3 block that TMA has brought: keys as they lie, values
+//               transposed (tokens in a row), both in the 128-byte swizzle that the
+//               tensor cores read;
+//   warp 8      one thread issues the products: S = Q K^T into one of two places,
+//               then O += P V of the block before.
+// A softmax thread reads its scores twice, for the maximum and for the probabilities:
+// two CTAs of 9 warps leave 96 registers a thread.
+// Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
+// tiles begin and end; a tile cut between CTAs is finished by the last to arrive.
+#include "attn_kv8.cuh"
+
+namespace patch {
+namespace attn {
+
+struct RowsParams {
+  CUtensorMap k_map, v_map;
+  AttnParams a;
+  uint32_t* counters;  // one per CTA
+  float* parts;        // two tile states per CTA
+  uint64_t limit_ns;
+  int page_shift, box_shift;
+};
+
+template <int D>
+struct RowsCfg {
+  static constexpr int CH = 64, R = 128;  // tokens of a block, rows of a tile
+  static constexpr int kWarps = 9, kThreads = 32 * kWarps;
+  static constexpr int kRawBytes = CH * D;
+  static constexpr int kQ = 0;                          // [D / 64][128 rows][128 bytes], swizzled
+  static constexpr int kK = kQ + R * D * 2;             // [D / 64][64 tokens][128 bytes]
+  static constexpr int kV = kK + CH * D * 2;            // [D][64 tokens]
+  static constexpr int kP = kV + CH * D * 2;            // [128 rows][64 tokens]
+  static constexpr int kRawK = kP + R * CH * 2;         // e4m3 as in the cache
+  static constexpr int kRawV = kRawK + kRawBytes;
+  static constexpr int kNan = kRawV + kRawBytes;        // 2 x [64 tokens][4 words]: elements of a token that are NaN
+  static constexpr int kBars = kNan + 2 * CH * 16;
+  static constexpr int kMisc = kBars + 128;
+  static constexpr int kSmem = kMisc + 256;
+  static constexpr int kStateFloats = R * D + 2 * R;    // o (in groups of 4 columns), m, l
+  static constexpr uint32_t kTmemCols = 256, kO = 128;  // S at 0 and 64, O from 128 on
+};
+
+constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
+  using C = RowsCfg<D>;
+  constexpr int CH = C::CH, R = C::R;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const AttnParams& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.heads / a.kv_heads;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint64_t *raw_k = bars, *raw_v = bars + 1;       // a block has landed
+  uint64_t *k_full = bars + 2, *v_full = bars + 3; // converted
+  uint64_t* s_full = bars + 4;                     // [2] scores done (K may be written again)
+  uint64_t* s_free = bars + 6;                     // [2] scores read
+  uint64_t *p_full = bars + 8, *o_done = bars + 9; // probabilities written; O += P V done (P and V may be written again)
+  uint64_t *q_full = bars + 10, *drain = bars + 11;
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 14 words
+  int* abort_flag = reinterpret_cast<int*>(misc + 16);
+  int* last_flag = abort_flag + 1;
+  int* nan_block = abort_flag + 2;  // [2] 1 + number of the block whose NaN masks are valid
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 4);
+  if (threadIdx.x == 0) {
+    const int counts[12] = {1, 1, 1, 1, 1, 1, 4, 4, 4, 1, 4, 1};
+    for (int i = 0; i < 12; ++i) tc::mbar_init(bars + i, counts[i]);
+    tc::fence_barrier_init();
+    *abort_flag = 0;
+    nan_block[0] = nan_block[1] = 0;
+    tc::prefetch_tensormap(&P.k_map);
+    tc::prefetch_tensormap(&P.v_map);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Share sh;
+  if (!make_share<CH, R, C::kWarps, 1>(a, G, misc, sh)) return;
+  if (warp == 8) tc::tmem_alloc(tmem_at, C::kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return tc::wait_bounded(bar, parity & 1, abort_flag, P.limit_ns, a.status, false);
+  };
+  // every role walks the same blocks: g counts them over the CTA's whole share
+  Cursor cur{};
+  cur.start<CH, R>(a, G, misc + C::kWarps, sh.u0, sh.u0 + sh.u_n);
+  const int64_t v1 = sh.u0 + sh.u_n;
+
+  if (warp < 4) {
+    // ================= softmax: thread = row of the tile
+    const int row = threadIdx.x;
+    const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
+    int g = 0;
+    for (; cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
+      const Tile& t = cur.t;
+      // ---- this row's query, divided by a power of two, to shared memory
+      const int r = t.rt * R + row;
+      const bool live = r < t.m * G;
+      const int64_t at = t.row0 + r / G;
+      const int head = t.h * G + r % G;
+      float row_scale;
+      {
+        const T* src = static_cast<const T*>(a.q) + at * a.q_ts + head * a.q_hs;
+        float amax = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          float x[8];
+          if (live) {
+            load16(src + 8 * i, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+          }
+        }
+        const uint32_t ex = __float_as_uint(amax) >> 23;
+        const bool plain = ex == 0 || ex >= 254;
+        // a negative scale turns the query round, so that maxima of products are maxima of scores
+        const float down = (plain ? 1.0f : __uint_as_float((254 - ex) << 23)) * (a.scale < 0.0f ? -1.0f : 1.0f);
+        row_scale = (plain ? 1.0f : __uint_as_float(ex << 23)) * (fabsf(a.scale) * kLog2e);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          float x[8];
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) {
+            load16(src + 8 * i, x);
+            v.x = pack_f16(x[0] * down, x[1] * down);
+            v.y = pack_f16(x[2] * down, x[3] * down);
+            v.z = pack_f16(x[4] * down, x[5] * down);
+            v.w = pack_f16(x[6] * down, x[7] * down);
+          }
+          *reinterpret_cast<uint4*>(smem + C::kQ + (i >> 3) * (R * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v;
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+      const int pos = t.len - t.m + r / G;
+      const int see_hi = live ? (a.causal ? min(t.len, pos + 1) : t.len) : 0;
+      const int see_lo = a.window > 0 ? int(max(int64_t(0), pos - a.window + 1)) : 0;
+      const int all_hi = a.causal ? t.len - t.m + t.rt * R / G + 1 : t.len;
+      const int last_row = min(t.m - 1, (t.rt * R + R - 1) / G);
+      const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
+
+      // scales of a block's pages: lane i has those of 16-token slice i (i < 4)
+      auto load_scales = [&](int c, float& ks, float& vs) {
+        ks = 1.0f;
+        vs = 0.0f;
+        const int tok = (t.chunk0 + c) * CH + 16 * (lane & 3);
+        if (tok < t.hi) {
+          const int phys = a.block_table[t.b * a.max_pages + (tok >> P.page_shift)];
+          if (phys >= 0 && phys < a.n_pages) {
+            const int64_t blk = int64_t(phys) * a.kv_heads + t.h;
+            ks = a.k_scale[blk];
+            vs = a.v_scale[blk];
+          }
+        }
+      };
+      float ks_next, vs_next;
+      load_scales(cur.c, ks_next, vs_next);
+
+      float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;
+      uint32_t nan_row[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) nan_row[i] = 0;
+      // what block g - 1's NaN values mean for this row (its values have been converted by now)
+      auto see_nan = [&](int c, int g_of) {
+        if (nan_block[g_of & 1] != g_of + 1) return;
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kNan + (g_of & 1) * CH * 16);
+        const int t0 = (t.chunk0 + c) * CH;
+        for (int k = max(0, see_lo - t0); k < min(CH, see_hi - t0); ++k)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) nan_row[i] |= mask[4 * k + i];
+      };
+      bool ok = true;
+      for (int c = cur.c; c < cur.c_end; ++c, ++g) {
+        const bool first = c == cur.c;
+        const float ks_lane = ks_next, vs_lane = vs_next;
+        if (c + 1 < cur.c_end) load_scales(c + 1, ks_next, vs_next);
+        ok = wait(s_full + (g & 1), g >> 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const int t0 = (t.chunk0 + c) * CH;
+        const bool some_hidden = t0 + CH > all_hi || t0 < all_lo;
+        const uint32_t s_at = lanes + (g & 1) * CH;
+        // 32 scores, as products; hidden ones -inf
+        auto scores = [&](int j0, float (&s)[32]) {
+          tc::tmem_ld_32cols(s_at + j0, reinterpret_cast<uint32_t(&)[32]>(s));
+          if (some_hidden) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (t0 + j0 + j >= see_hi || t0 + j0 + j < see_lo) s[j] = -INFINITY;
+          }
+        };
+        float kc[4], vs[4], mx = m, v_new = v_ref;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          kc[i] = fmaxf(__shfl_sync(0xFFFFFFFFu, ks_lane, i) * row_scale, 1.0e-37f);  // not 0: hidden scores are -inf times it
+          vs[i] = __shfl_sync(0xFFFFFFFFu, vs_lane, i);
+          v_new = fmaxf(v_new, vs[i]);
+        }
+#pragma unroll
+        for (int j0 = 0; j0 < CH; j0 += 32) {
+          float s[32];
+          scores(j0, s);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = s[16 * i];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, s[16 * i + j]);
+            if (top != -INFINITY) mx = fmaxf(mx, top * kc[j0 / 16 + i]);
+          }
+        }
+        // P and O are this thread's again once the block before has been added
+        if (!first) {
+          ok = wait(o_done, g - 1);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          see_nan(c - 1, g - 1);
+        }
+        const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
+        if (__any_sync(0xFFFFFFFFu, grow || v_new != v_ref)) {
+          const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
+          if (grow) m = mx;
+          l *= f;
+          if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
+          const float fo = f * (v_ref * v_inv);
+          v_ref = v_new;
+          if (!first) {
+#pragma unroll
+            for (int j = 0; j < D; j += 32) {
+              uint32_t o[32];
+              tc::tmem_ld_32cols(lanes + C::kO + j, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
+              tmem_st_32cols(lanes + C::kO + j, o);
+            }
+            tc::tmem_wait_st();
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int j0 = 0; j0 < CH; j0 += 32) {
+          float s[32];
+          scores(j0, s);
+          if (j0 + 32 == CH) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(s_free + (g & 1));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float k = kc[j0 / 16 + i], vr = vs[j0 / 16 + i] * v_inv;
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float s0 = s[16 * i + 2 * j], s1 = s[16 * i + 2 * j + 1];
+              const float p0 = ex2(fmaf(s0, k, -base)), p1 = ex2(fmaf(s1, k, -base));
+              l += p0 + p1;
+              w[j] = pack_f16(p0 * vr, p1 * vr);
+            }
+            uint8_t* dst = smem + C::kP + row * 128;
+            const int piece = j0 / 8 + 2 * i;
+            *reinterpret_cast<uint4*>(dst + ((piece ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + (((piece + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      // ---- the tile's sums over this CTA's blocks
+      ok = wait(o_done, g - 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc::tc_fence_after();
+      see_nan(cur.c_end - 1, g - 1);
+      const bool whole = cur.c == 0 && cur.c_end == t.chunks;
+      float* part = P.parts + (2 * blockIdx.x + (cur.c == 0 ? 1 : 0)) * int64_t(C::kStateFloats);
+      T* dst = static_cast<T*>(a.out) + at * a.o_ts + head * a.o_hs;
+      auto write_lse = [&](float m_, float l_) {
+        if (a.lse && live)
+          a.lse[at * a.heads + head] = m_ == -INFINITY && l_ == 0.0f ? -INFINITY : (m_ + log2f(l_)) / kLog2e;
+      };
+      const float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int j = 0; j < D; j += 32) {
+        uint32_t raw[32];
+        tc::tmem_ld_32cols(lanes + C::kO + j, raw);
+        float o[32];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          if (j == 32 * i) bad = nan_row[i];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          o[k] = __uint_as_float(raw[k]) * v_ref;
+          if (whole) o[k] *= inv;
+          if (bad >> k & 1) o[k] = __int_as_float(0x7FC00000);
+        }
+        if (whole) {
+          if (live)
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) store16(dst + j + k, o + k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + ((j + k) / 4 * R + row) * 4) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+      tc::tc_fence_before();
+      if (whole) {
+        write_lse(m, l);
+      } else {
+        part[R * D + row] = m;
+        part[R * D + R + row] = l;
+        const int64_t unit0 = v1 - cur.left;
+        const int64_t c0 = sh.owner(unit0 + kTileUnits), c1 = sh.owner(unit0 + kTileUnits + t.chunks - 1);
+        __threadfence();
+        tc::named_bar_sync(1, 128);
+        if (threadIdx.x == 0) {
+          const bool last = atomicAdd(P.counters + c0, 1u) == uint32_t(c1 - c0);
+          if (last) P.counters[c0] = 0;
+          *last_flag = last;
+        }
+        tc::named_bar_sync(1, 128);
+        if (*last_flag) {  // the last to arrive joins the parts, in CTA order
+          __threadfence();
+          auto part_of = [&](int64_t i) { return P.parts + (2 * i + (i == c0 ? 1 : 0)) * int64_t(C::kStateFloats); };
+          m = -INFINITY;
+          for (int64_t i = c0; i <= c1; ++i) m = fmaxf(m, __ldcg(part_of(i) + R * D + row));
+          const float base = m == -INFINITY ? 0.0f : m;
+          l = 0.0f;
+          for (int64_t i = c0; i <= c1; ++i)
+            l += __ldcg(part_of(i) + R * D + R + row) * ex2(__ldcg(part_of(i) + R * D + row) - base);
+          const float inv_all = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+          for (int j = 0; j < D; j += 32) {
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+            for (int64_t i = c0; i <= c1; ++i) {
+              const float* p = part_of(i);
+              const float f = ex2(__ldcg(p + R * D + row) - base);
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + ((j + k) / 4 * R + row) * 4));
+                o[k] += x.x * f;
+                o[k + 1] += x.y * f;
+                o[k + 2] += x.z * f;
+                o[k + 3] += x.w * f;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= inv_all;
+            if (live)
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) store16(dst + j + k, o + k);
+          }
+          write_lse(m, l);
+        }
+        tc::named_bar_sync(1, 128);  // the flag is read before the next cut tile writes it
+      }
+    }
+  } else if (warp < 8) {
+    // ================= conversion, and the loads of the next block
+    const int w = warp - 4;
+    int issued_k = 0, issued_v = 0, done_k = 0, done_v = 0;
+    Cursor kc = cur, vc = cur;  // what is loaded next of the keys, of the values
+    auto load = [&](Cursor& at_, const CUtensorMap* map, uint32_t dst, uint64_t* bar, int& issued) {  // warp 4
+      if (at_.c >= at_.c_end) return;
+      const Tile& t = at_.t;
+      const int t0 = (t.chunk0 + at_.c) * CH, box = 1 << P.box_shift;
+      const int n_box = min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift);
+      if (lane == 0) {
+        if (n_box > 0)
+          tc::mbar_expect_tx(bar, uint32_t(n_box) * uint32_t(D) << P.box_shift);
+        else
+          tc::mbar_arrive(bar);
+      }
+      __syncwarp();
+      if (lane < n_box) {
+        const int tok = t0 + (lane << P.box_shift);
+        const int phys = a.block_table[t.b * a.max_pages + (tok >> P.page_shift)];
+        const bool in = phys >= 0 && phys < a.n_pages;
+        if (!in) set_status(a.status, PATCH_DEV_BOUNDS);
+        const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
+        tma_load_3d(dst + lane * (D << P.box_shift), map, tc::smem_u32(bar), 0, tok & (a.page - 1), blk);
+      }
+      ++issued;
+      if (++at_.c == at_.c_end) at_.next<CH, R>(a, G);
+    };
+    const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
+    if (w == 0) {
+      load(kc, &P.k_map, raw_k_at, raw_k, issued_k);
+      load(vc, &P.v_map, raw_v_at, raw_v, issued_v);
+    }
+    // keys of block g: thread = token (two threads a token, half of its elements each)
+    auto convert_k = [&](int g) {
+      bool ok = wait(raw_k, g);
+      if (ok && g > 0) ok = wait(s_full + ((g - 1) & 1), (g - 1) >> 1);
+      ok = tc::named_bar_and(2, 128, ok);
+      if (!ok) return false;
+      const int tok = 32 * (w & 1) + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int p = (w >> 1) * (D / 32) + i;  // 16-byte piece of the row
+        const int at_ = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + C::kRawK + at_);
+        uint4 lo, hi;
+        cvt4(x.x, lo.x, lo.y);
+        cvt4(x.y, lo.z, lo.w);
+        cvt4(x.z, hi.x, hi.y);
+        cvt4(x.w, hi.z, hi.w);
+        uint8_t* dst = smem + C::kK + (p >> 2) * (CH * 128) + tok * 128;  // 64 elements a row
+        *reinterpret_cast<uint4*>(dst + (((2 * (p & 3)) ^ (tok & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(dst + (((2 * (p & 3) + 1) ^ (tok & 7)) << 4)) = hi;
+      }
+      tc::fence_proxy_async_smem();
+      tc::named_bar_sync(2, 128);
+      ++done_k;
+      if (w == 0) {
+        if (lane == 0) tc::mbar_arrive(k_full);
+        load(kc, &P.k_map, raw_k_at, raw_k, issued_k);
+      }
+      return true;
+    };
+    // values of block g: lane = two neighbouring tokens, 16 elements of each at a time
+    auto convert_v = [&](int g, int behind) {  // behind: tokens of the block before what no row sees
+      bool ok = wait(raw_v, g);
+      if (ok && g > 0) ok = wait(o_done, g - 1);
+      ok = tc::named_bar_and(2, 128, ok);
+      if (!ok) return false;
+      bool any = false;
+      uint32_t nan0[2] = {0, 0}, nan1[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int p = w * (D / 64) + i;
+        uint4 x[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int tok = 2 * lane + k;
+          const int at_ = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
+          x[k] = *reinterpret_cast<const uint4*>(smem + C::kRawV + at_);
+          if (tok >= behind) x[k] = make_uint4(0, 0, 0, 0);  // anything may lie there
+        }
+        uint32_t a0[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, a1[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
+        // NaN must not reach the rows that do not see its token (0 x NaN): kept as bits, and out of the product
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t n0 = __vcmpeq4(a0[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(a1[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          any |= (n0 | n1) != 0;
+          a0[j] &= ~n0;
+          a1[j] &= ~n1;
+          nan0[i & 1] |= ((n0 & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * j);
+          nan1[i & 1] |= ((n1 & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * j);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t e[4];  // elements 4 j .. 4 j + 3 of the piece, of both tokens
+          cvt4(__byte_perm(a0[j], a1[j], 0x5140), e[0], e[1]);
+          cvt4(__byte_perm(a0[j], a1[j], 0x7362), e[2], e[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int d = 16 * p + 4 * j + k;
+            *reinterpret_cast<uint32_t*>(smem + C::kV + d * 128 + (((lane >> 2) ^ (d & 7)) << 4) + (lane & 3) * 4) = e[k];
+          }
+        }
+      }
+      if (tc::named_bar_and(2, 128, !any) == false) {
+        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 1) * CH * 16);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          mask[(2 * lane) * 8 + w * (D / 64) + i] = uint16_t(nan0[i & 1]);
+          mask[(2 * lane + 1) * 8 + w * (D / 64) + i] = uint16_t(nan1[i & 1]);
+        }
+        if (w == 0 && lane == 0) nan_block[g & 1] = g + 1;
+      }
+      tc::fence_proxy_async_smem();
+      tc::named_bar_sync(2, 128);
+      ++done_v;
+      if (w == 0) {
+        if (lane == 0) tc::mbar_arrive(v_full);
+        load(vc, &P.v_map, raw_v_at, raw_v, issued_v);
+      }
+      return true;
+    };
+    int g = 0;
+    bool ok = cur.c < cur.c_end && convert_k(0);
+    // keys run a block ahead of values
+    while (ok && cur.c < cur.c_end) {
+      const int behind = cur.t.hi - (cur.t.chunk0 + cur.c) * CH;
+      if (++cur.c == cur.c_end) cur.next<CH, R>(a, G);
+      if (cur.c < cur.c_end) ok = convert_k(g + 1);
+      ok = ok && convert_v(g, behind);
+      ++g;
+    }
+    if (w == 0) {  // after a timeout: let the copies in flight land
+      for (; done_k < issued_k; ++done_k) tc::wait_bounded(raw_k, done_k & 1, abort_flag, P.limit_ns, a.status, true);
+      for (; done_v < issued_v; ++done_v) tc::wait_bounded(raw_v, done_v & 1, abort_flag, P.limit_ns, a.status, true);
+    }
+  } else if (lane == 0) {
+    // ================= the products
+    const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(smem + C::kQ)), k_desc = tc::sw128_desc(tc::smem_u32(smem + C::kK));
+    const uint64_t p_desc = tc::sw128_desc(tc::smem_u32(smem + C::kP)), v_desc = tc::sw128_desc(tc::smem_u32(smem + C::kV));
+    auto product_pv = [&](int g, bool first) {
+      if (!wait(v_full, g) || !wait(p_full, g)) return false;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < CH / 16; ++k)  // 16 tokens are 32 bytes of a row
+        tc::mma_dense(tmem + C::kO, p_desc + 2 * k, v_desc + 2 * k, idesc_f16(R, D), !first || k > 0);
+      tc::tc_commit(o_done);
+      return true;
+    };
+    int g = 0, tiles = 0;
+    bool ok = true, first_pending = false;
+    for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G), ++tiles) {
+      for (int c = cur.c; ok && c < cur.c_end; ++c, ++g) {
+        const bool first = c == cur.c;
+        if (first && g > 0) ok = product_pv(g - 1, first_pending);  // the last tile's; its sums are read before Q changes
+        ok = ok && wait(k_full, g) && (g < 2 || wait(s_free + (g & 1), (g - 2) >> 1)) && (!first || wait(q_full, tiles));
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_dense(tmem + (g & 1) * CH, q_desc + (k >> 2) * (R * 128 / 16) + 2 * (k & 3),
+                        k_desc + (k >> 2) * (CH * 128 / 16) + 2 * (k & 3), idesc_f16(R, CH), k > 0);
+        tc::tc_commit(s_full + (g & 1));
+        if (!first) ok = product_pv(g - 1, first_pending);
+        first_pending = first;
+      }
+    }
+    if (ok && g > 0) product_pv(g - 1, first_pending);
+    tc::tc_commit(drain);  // nothing in flight when the memory goes
+    tc::wait_bounded(drain, 0, abort_flag, P.limit_ns, a.status, true);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 8) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <typename T, int D>
+static cudaError_t launch_rows(const RowsParams& P, int ctas, cudaStream_t stream) {
+  constexpr int kSmem = RowsCfg<D>::kSmem;
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+  auto kernel = attn_kv8_rows_kernel<T, D>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(unsigned(ctas)), dim3(RowsCfg<D>::kThreads), kSmem, stream, P);
+}
+
+}  // namespace attn
+
+// Counters for two CTAs per SM, then the tile states of as many CTAs as there is room for, one per SM at least.
+static size_t rows_counter_bytes(int num_sms) { return (size_t(num_sms) * 8 + 255) / 256 * 256; }
+static size_t rows_state_bytes(int64_t head_dim) {
+  return 2 * 4 * size_t(head_dim == 128 ? attn::RowsCfg<128>::kStateFloats : attn::RowsCfg<64>::kStateFloats);
+}
+size_t attn_kv8_rows_workspace_bytes(int64_t head_dim, int num_sms) {
+  return rows_counter_bytes(num_sms) + num_sms * rows_state_bytes(head_dim);
+}
+
+cudaError_t launch_attn_kv8_rows(const AttnParams& a, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
+                                 int num_sms, uint64_t limit_ns, cudaStream_t stream) {
+  attn::RowsParams P = {};
+  P.a = a;
+  P.counters = static_cast<uint32_t*>(workspace);
+  P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rows_counter_bytes(num_sms));
+  P.limit_ns = limit_ns;
+  const int box = a.page < 64 ? a.page : 64;
+  for (P.page_shift = 4; (1 << P.page_shift) < a.page;) ++P.page_shift;
+  for (P.box_shift = 4; (1 << P.box_shift) < box;) ++P.box_shift;
+  if (!make_map_pages_u8(&P.k_map, a.k, head_dim, a.page, a.n_pages * a.kv_heads, box) ||
+      !make_map_pages_u8(&P.v_map, a.v, head_dim, a.page, a.n_pages * a.kv_heads, box))
+    return cudaErrorInvalidValue;
+  int64_t ctas = int64_t((workspace_bytes - rows_counter_bytes(num_sms)) / rows_state_bytes(head_dim));
+  if (ctas > 2 * int64_t(num_sms)) ctas = 2 * int64_t(num_sms);
+  if (dtype == PATCH_DTYPE_BF16)
+    return head_dim == 128 ? attn::launch_rows<__nv_bfloat16, 128>(P, int(ctas), stream)
+                           : attn::launch_rows<__nv_bfloat16, 64>(P, int(ctas), stream);
+  return head_dim == 128 ? attn::launch_rows<__half, 128>(P, int(ctas), stream)
+                         : attn::launch_rows<__half, 64>(P, int(ctas), stream);
+}
+
+}  // namespace patch
