@@ -8,18 +8,18 @@
 // about 2 x 256 tensor-core cycles (D = 128), 512 cycles of exponentials and some
 // 700 of other softmax instructions, so the roles run side by side, and two CTAs
 // share an SM:
-//   warps 0-3   softmax, a thread per row: scores from tensor memory, the running
-//               maximum, probabilities as fp16 to shared memory.  The sum of the
-//               values stays in tensor memory and is rescaled only when a row's
-//               maximum grows by more than 2^8 (probabilities are at most 2^8 then,
-//               well inside fp16, and the sums are fp32);
+//   warps 0-3   softmax, a thread per row: scores from tensor memory (read twice, for
+//               the maximum and for the probabilities: two CTAs leave 96 registers a
+//               thread), probabilities as fp16 back into the place of the scores, where
+//               the second product takes them.  The sum of the values stays in tensor
+//               memory and is rescaled only when a row's maximum grows by more than 2^8
+//               (probabilities are at most 2^8 then, well inside fp16; sums are fp32);
 //   warps 4-7   convert the e4m3 block that TMA has brought: keys as they lie, values
 //               transposed (tokens in a row), both in the 128-byte swizzle that the
 //               tensor cores read;
-//   warp 8      one thread issues the products: S = Q K^T into one of two places,
-//               then O += P V of the block before.
-// A softmax thread reads its scores twice, for the maximum and for the probabilities:
-// two CTAs of 9 warps leave 96 registers a thread.
+//   warp 8      one thread issues the products: S = Q K^T for block g into one of two
+//               places once O += P V of block g - 2, which held that place, is done;
+//   warp 9      fetches: block table, scales, TMA.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
 // tiles begin and end; a tile cut between CTAs is finished by the last to arrive.
 #include "attn_kv8.cuh"
@@ -39,20 +39,20 @@ struct RowsParams {
 template <int D>
 struct RowsCfg {
   static constexpr int CH = 64, R = 128;  // tokens of a block, rows of a tile
-  static constexpr int kWarps = 9, kThreads = 32 * kWarps;
+  static constexpr int kWarps = 10, kThreads = 32 * kWarps;
   static constexpr int kRawBytes = CH * D;
-  static constexpr int kQ = 0;                          // [D / 64][128 rows][128 bytes], swizzled
-  static constexpr int kK = kQ + R * D * 2;             // [D / 64][64 tokens][128 bytes]
-  static constexpr int kV = kK + CH * D * 2;            // [D][64 tokens]
-  static constexpr int kP = kV + CH * D * 2;            // [128 rows][64 tokens]
-  static constexpr int kRawK = kP + R * CH * 2;         // e4m3 as in the cache
-  static constexpr int kRawV = kRawK + kRawBytes;
-  static constexpr int kNan = kRawV + kRawBytes;        // 2 x [64 tokens][4 words]: elements of a token that are NaN
-  static constexpr int kBars = kNan + 2 * CH * 16;
-  static constexpr int kMisc = kBars + 128;
+  static constexpr int kQ = 0;                      // [D / 64][128 rows][128 bytes], swizzled
+  static constexpr int kK = kQ + R * D * 2;         // [D / 64][64 tokens][128 bytes]
+  static constexpr int kV = kK + CH * D * 2;        // 2 x [D][64 tokens]
+  static constexpr int kRawK = kV + 2 * CH * D * 2;  // 2 x e4m3 as in the cache
+  static constexpr int kRawV = kRawK + 2 * kRawBytes;
+  static constexpr int kNan = kRawV + kRawBytes;    // 4 x [64 tokens][4 words]: elements of a token that are NaN
+  static constexpr int kScales = kNan + 4 * CH * 16;  // 8 x [4 slices of 16 tokens] (key, value) scales
+  static constexpr int kBars = kScales + 8 * 32;
+  static constexpr int kMisc = kBars + 256;
   static constexpr int kSmem = kMisc + 256;
   static constexpr int kStateFloats = R * D + 2 * R;    // o (in groups of 4 columns), m, l
-  static constexpr uint32_t kTmemCols = 256, kO = 128;  // S at 0 and 64, O from 128 on
+  static constexpr uint32_t kTmemCols = 256, kO = 128;  // S and P at 0 and 64, O from 128 on
 };
 
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
@@ -72,6 +72,24 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+// the A operand in tensor memory: lane = row, a column holds two neighbouring fp16 of k
+__device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
   using C = RowsCfg<D>;
@@ -81,23 +99,27 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.heads / a.kv_heads;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
-  uint64_t *raw_k = bars, *raw_v = bars + 1;       // a block has landed
-  uint64_t *k_full = bars + 2, *v_full = bars + 3; // converted
-  uint64_t* s_full = bars + 4;                     // [2] scores done (K may be written again)
-  uint64_t* s_free = bars + 6;                     // [2] scores read
-  uint64_t *p_full = bars + 8, *o_done = bars + 9; // probabilities written; O += P V done (P and V may be written again)
-  uint64_t *q_full = bars + 10, *drain = bars + 11;
-  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 14 words
+  // Barriers of the pipeline.  Those with two or more places take blocks in turn, so that no
+  // waiter is ever two phases behind.
+  uint64_t *raw_k = bars, *raw_k_free = bars + 2;           // [2] key bytes landed, read
+  uint64_t *raw_v = bars + 4, *raw_v_free = bars + 5;       // value bytes landed, read
+  uint64_t *k_full = bars + 6, *v_full = bars + 7;          // converted; values [2]
+  uint64_t* s_full = bars + 9;                              // [2] scores done (the keys may be written again)
+  uint64_t* p_full = bars + 11;                             // [2] probabilities written
+  uint64_t* o_done = bars + 13;                             // [2] O += P V done
+  uint64_t *q_full = bars + 15, *drain = bars + 16;
+  uint64_t* scales_full = bars + 17;                        // [8]
+  float2* scales = reinterpret_cast<float2*>(smem + C::kScales);
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 12 words
   int* abort_flag = reinterpret_cast<int*>(misc + 16);
   int* last_flag = abort_flag + 1;
-  int* nan_block = abort_flag + 2;  // [2] 1 + number of the block whose NaN masks are valid
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 4);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 2);
+  int* nan_block = abort_flag + 4;  // [4] 1 + number of the block whose NaN masks are valid
   if (threadIdx.x == 0) {
-    const int counts[12] = {1, 1, 1, 1, 1, 1, 4, 4, 4, 1, 4, 1};
-    for (int i = 0; i < 12; ++i) tc::mbar_init(bars + i, counts[i]);
+    for (int i = 0; i < 25; ++i) tc::mbar_init(bars + i, i == 11 || i == 12 || i == 15 ? 4 : 1);
     tc::fence_barrier_init();
     *abort_flag = 0;
-    nan_block[0] = nan_block[1] = 0;
+    for (int i = 0; i < 4; ++i) nan_block[i] = 0;
     tc::prefetch_tensormap(&P.k_map);
     tc::prefetch_tensormap(&P.v_map);
   }
@@ -171,31 +193,14 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       const int last_row = min(t.m - 1, (t.rt * R + R - 1) / G);
       const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
 
-      // scales of a block's pages: lane i has those of 16-token slice i (i < 4)
-      auto load_scales = [&](int c, float& ks, float& vs) {
-        ks = 1.0f;
-        vs = 0.0f;
-        const int tok = (t.chunk0 + c) * CH + 16 * (lane & 3);
-        if (tok < t.hi) {
-          const int phys = a.block_table[t.b * a.max_pages + (tok >> P.page_shift)];
-          if (phys >= 0 && phys < a.n_pages) {
-            const int64_t blk = int64_t(phys) * a.kv_heads + t.h;
-            ks = a.k_scale[blk];
-            vs = a.v_scale[blk];
-          }
-        }
-      };
-      float ks_next, vs_next;
-      load_scales(cur.c, ks_next, vs_next);
-
       float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;
       uint32_t nan_row[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) nan_row[i] = 0;
-      // what block g - 1's NaN values mean for this row (its values have been converted by now)
+      // what a block's NaN values mean for this row (once the block's values have been converted)
       auto see_nan = [&](int c, int g_of) {
-        if (nan_block[g_of & 1] != g_of + 1) return;
-        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kNan + (g_of & 1) * CH * 16);
+        if (nan_block[g_of & 3] != g_of + 1) return;
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kNan + (g_of & 3) * CH * 16);
         const int t0 = (t.chunk0 + c) * CH;
         for (int k = max(0, see_lo - t0); k < min(CH, see_hi - t0); ++k)
 #pragma unroll
@@ -204,14 +209,13 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       bool ok = true;
       for (int c = cur.c; c < cur.c_end; ++c, ++g) {
         const bool first = c == cur.c;
-        const float ks_lane = ks_next, vs_lane = vs_next;
-        if (c + 1 < cur.c_end) load_scales(c + 1, ks_next, vs_next);
-        ok = wait(s_full + (g & 1), g >> 1);
+        ok = wait(scales_full + (g & 7), g >> 3) && wait(s_full + (g & 1), g >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
+        if (c - 2 >= cur.c) see_nan(c - 2, g - 2);  // these scores have taken the place of its probabilities
         const int t0 = (t.chunk0 + c) * CH;
         const bool some_hidden = t0 + CH > all_hi || t0 < all_lo;
         const uint32_t s_at = lanes + (g & 1) * CH;
@@ -227,8 +231,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
         float kc[4], vs[4], mx = m, v_new = v_ref;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          kc[i] = fmaxf(__shfl_sync(0xFFFFFFFFu, ks_lane, i) * row_scale, 1.0e-37f);  // not 0: hidden scores are -inf times it
-          vs[i] = __shfl_sync(0xFFFFFFFFu, vs_lane, i);
+          const float2 sc = scales[4 * (g & 7) + i];
+          kc[i] = fmaxf(sc.x * row_scale, 1.0e-37f);  // not 0: hidden scores are -inf times it
+          vs[i] = sc.y;
           v_new = fmaxf(v_new, vs[i]);
         }
 #pragma unroll
@@ -243,16 +248,6 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
             if (top != -INFINITY) mx = fmaxf(mx, top * kc[j0 / 16 + i]);
           }
         }
-        // P and O are this thread's again once the block before has been added
-        if (!first) {
-          ok = wait(o_done, g - 1);
-          if (!__all_sync(0xFFFFFFFFu, ok)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          see_nan(c - 1, g - 1);
-        }
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, grow || v_new != v_ref)) {
           const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
@@ -261,8 +256,10 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
           const float fo = f * (v_ref * v_inv);
           v_ref = v_new;
-          if (!first) {
-#pragma unroll
+          if (!first) {  // O is this thread's once the block before has been added
+            ok = __all_sync(0xFFFFFFFFu, wait(o_done + ((g - 1) & 1), (g - 1) >> 1));
+            tc::tc_fence_after();
+#pragma unroll 1
             for (int j = 0; j < D; j += 32) {
               uint32_t o[32];
               tc::tmem_ld_32cols(lanes + C::kO + j, o);
@@ -278,38 +275,31 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
         for (int j0 = 0; j0 < CH; j0 += 32) {
           float s[32];
           scores(j0, s);
-          if (j0 + 32 == CH) {
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(s_free + (g & 1));
-          }
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float k = kc[j0 / 16 + i], vr = vs[j0 / 16 + i] * v_inv;
-            uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float s0 = s[16 * i + 2 * j], s1 = s[16 * i + 2 * j + 1];
               const float p0 = ex2(fmaf(s0, k, -base)), p1 = ex2(fmaf(s1, k, -base));
               l += p0 + p1;
-              w[j] = pack_f16(p0 * vr, p1 * vr);
+              w[8 * i + j] = pack_f16(p0 * vr, p1 * vr);
             }
-            uint8_t* dst = smem + C::kP + row * 128;
-            const int piece = j0 / 8 + 2 * i;
-            *reinterpret_cast<uint4*>(dst + ((piece ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + (((piece + 1) ^ (row & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
+          tmem_st_16cols(s_at + j0 / 2, w);  // over scores that have been read
         }
-        tc::fence_proxy_async_smem();
+        tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full);
+        if (lane == 0) tc::mbar_arrive(p_full + (g & 1));
       }
       if (!ok) break;
       // ---- the tile's sums over this CTA's blocks
-      ok = wait(o_done, g - 1);
+      ok = wait(o_done + ((g - 1) & 1), (g - 1) >> 1);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc::tc_fence_after();
+      if (cur.c_end - 2 >= cur.c) see_nan(cur.c_end - 2, g - 2);
       see_nan(cur.c_end - 1, g - 1);
       const bool whole = cur.c == 0 && cur.c_end == t.chunks;
       float* part = P.parts + (2 * blockIdx.x + (cur.c == 0 ? 1 : 0)) * int64_t(C::kStateFloats);
@@ -399,50 +389,21 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       }
     }
   } else if (warp < 8) {
-    // ================= conversion, and the loads of the next block
+    // ================= conversion
     const int w = warp - 4;
-    int issued_k = 0, issued_v = 0, done_k = 0, done_v = 0;
-    Cursor kc = cur, vc = cur;  // what is loaded next of the keys, of the values
-    auto load = [&](Cursor& at_, const CUtensorMap* map, uint32_t dst, uint64_t* bar, int& issued) {  // warp 4
-      if (at_.c >= at_.c_end) return;
-      const Tile& t = at_.t;
-      const int t0 = (t.chunk0 + at_.c) * CH, box = 1 << P.box_shift;
-      const int n_box = min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift);
-      if (lane == 0) {
-        if (n_box > 0)
-          tc::mbar_expect_tx(bar, uint32_t(n_box) * uint32_t(D) << P.box_shift);
-        else
-          tc::mbar_arrive(bar);
-      }
-      __syncwarp();
-      if (lane < n_box) {
-        const int tok = t0 + (lane << P.box_shift);
-        const int phys = a.block_table[t.b * a.max_pages + (tok >> P.page_shift)];
-        const bool in = phys >= 0 && phys < a.n_pages;
-        if (!in) set_status(a.status, PATCH_DEV_BOUNDS);
-        const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
-        tma_load_3d(dst + lane * (D << P.box_shift), map, tc::smem_u32(bar), 0, tok & (a.page - 1), blk);
-      }
-      ++issued;
-      if (++at_.c == at_.c_end) at_.next<CH, R>(a, G);
-    };
-    const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
-    if (w == 0) {
-      load(kc, &P.k_map, raw_k_at, raw_k, issued_k);
-      load(vc, &P.v_map, raw_v_at, raw_v, issued_v);
-    }
     // keys of block g: thread = token (two threads a token, half of its elements each)
     auto convert_k = [&](int g) {
-      bool ok = wait(raw_k, g);
+      bool ok = wait(raw_k + (g & 1), g >> 1);
       if (ok && g > 0) ok = wait(s_full + ((g - 1) & 1), (g - 1) >> 1);
       ok = tc::named_bar_and(2, 128, ok);
       if (!ok) return false;
       const int tok = 32 * (w & 1) + lane;
+      const uint8_t* raw = smem + C::kRawK + (g & 1) * C::kRawBytes;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int p = (w >> 1) * (D / 32) + i;  // 16-byte piece of the row
-        const int at_ = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
-        const uint4 x = *reinterpret_cast<const uint4*>(smem + C::kRawK + at_);
+        const int at = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + at);
         uint4 lo, hi;
         cvt4(x.x, lo.x, lo.y);
         cvt4(x.y, lo.z, lo.w);
@@ -454,17 +415,16 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       }
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(2, 128);
-      ++done_k;
-      if (w == 0) {
-        if (lane == 0) tc::mbar_arrive(k_full);
-        load(kc, &P.k_map, raw_k_at, raw_k, issued_k);
+      if (threadIdx.x == 128) {
+        tc::mbar_arrive(k_full);
+        tc::mbar_arrive(raw_k_free + (g & 1));
       }
       return true;
     };
     // values of block g: lane = two neighbouring tokens, 16 elements of each at a time
     auto convert_v = [&](int g, int behind) {  // behind: tokens of the block before what no row sees
       bool ok = wait(raw_v, g);
-      if (ok && g > 0) ok = wait(o_done, g - 1);
+      if (ok && g > 1) ok = wait(o_done + (g & 1), (g - 2) >> 1);
       ok = tc::named_bar_and(2, 128, ok);
       if (!ok) return false;
       bool any = false;
@@ -476,8 +436,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int tok = 2 * lane + k;
-          const int at_ = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
-          x[k] = *reinterpret_cast<const uint4*>(smem + C::kRawV + at_);
+          const int at = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
+          x[k] = *reinterpret_cast<const uint4*>(smem + C::kRawV + at);
           if (tok >= behind) x[k] = make_uint4(0, 0, 0, 0);  // anything may lie there
         }
         uint32_t a0[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, a1[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
@@ -485,7 +445,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t n0 = __vcmpeq4(a0[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(a1[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          any |= (n0 | n1) != 0;
+          if ((n0 | n1) == 0) continue;
+          any = true;
           a0[j] &= ~n0;
           a1[j] &= ~n1;
           nan0[i & 1] |= ((n0 & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * j);
@@ -496,65 +457,115 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           uint32_t e[4];  // elements 4 j .. 4 j + 3 of the piece, of both tokens
           cvt4(__byte_perm(a0[j], a1[j], 0x5140), e[0], e[1]);
           cvt4(__byte_perm(a0[j], a1[j], 0x7362), e[2], e[3]);
+          uint8_t* dst = smem + C::kV + (g & 1) * (CH * D * 2) + (16 * p + 4 * j) * 128 + (lane & 3) * 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int d = 16 * p + 4 * j + k;
-            *reinterpret_cast<uint32_t*>(smem + C::kV + d * 128 + (((lane >> 2) ^ (d & 7)) << 4) + (lane & 3) * 4) = e[k];
-          }
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint32_t*>(dst + k * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
         }
       }
-      if (tc::named_bar_and(2, 128, !any) == false) {
-        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 1) * CH * 16);
+      if (!tc::named_bar_and(2, 128, !any)) {
+        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 3) * CH * 16);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           mask[(2 * lane) * 8 + w * (D / 64) + i] = uint16_t(nan0[i & 1]);
           mask[(2 * lane + 1) * 8 + w * (D / 64) + i] = uint16_t(nan1[i & 1]);
         }
-        if (w == 0 && lane == 0) nan_block[g & 1] = g + 1;
+        if (threadIdx.x == 128) nan_block[g & 3] = g + 1;
       }
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(2, 128);
-      ++done_v;
-      if (w == 0) {
-        if (lane == 0) tc::mbar_arrive(v_full);
-        load(vc, &P.v_map, raw_v_at, raw_v, issued_v);
+      if (threadIdx.x == 128) {
+        tc::mbar_arrive(v_full + (g & 1));
+        tc::mbar_arrive(raw_v_free);
       }
       return true;
     };
     int g = 0;
-    bool ok = cur.c < cur.c_end && convert_k(0);
-    // keys run a block ahead of values
-    while (ok && cur.c < cur.c_end) {
-      const int behind = cur.t.hi - (cur.t.chunk0 + cur.c) * CH;
-      if (++cur.c == cur.c_end) cur.next<CH, R>(a, G);
-      if (cur.c < cur.c_end) ok = convert_k(g + 1);
-      ok = ok && convert_v(g, behind);
-      ++g;
+    for (bool ok = true; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G))
+      for (int c = cur.c; ok && c < cur.c_end; ++c, ++g)
+        ok = convert_k(g) && convert_v(g, cur.t.hi - (cur.t.chunk0 + c) * CH);
+  } else if (warp == 9) {
+    // ================= loads: lane i < 4 has the 16-token slice i of a block
+    const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
+    int g = 0;
+    bool ok = true;
+    for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
+      const Tile& t = cur.t;
+      auto page_of = [&](int c) {
+        const int tok = (t.chunk0 + c) * CH + 16 * (lane & 3);
+        return lane < 4 && tok < t.hi ? a.block_table[t.b * a.max_pages + (tok >> P.page_shift)] : -1;
+      };
+      int next = page_of(cur.c);
+      for (int c = cur.c; c < cur.c_end; ++c, ++g) {
+        const int t0 = (t.chunk0 + c) * CH, tok = t0 + 16 * (lane & 3), phys = next;
+        if (c + 1 < cur.c_end) next = page_of(c + 1);
+        const int box = 1 << P.box_shift;
+        const int n_box = max(min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift), 0);
+        const uint32_t bytes = uint32_t(n_box * D) << P.box_shift;
+        const bool in = phys >= 0 && phys < a.n_pages, wanted = lane < 4 && tok < t.hi;
+        if (wanted && !in) set_status(a.status, PATCH_DEV_BOUNDS);
+        const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
+        const bool leads = wanted && (16 * lane & (box - 1)) == 0;
+        auto issue = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
+          if (lane == 0) {
+            if (n_box > 0)
+              tc::mbar_expect_tx(bar, bytes);
+            else
+              tc::mbar_arrive(bar);
+          }
+          __syncwarp();
+          if (leads) tma_load_3d(dst + 16 * lane * D, map, tc::smem_u32(bar), 0, tok & (a.page - 1), blk);
+        };
+        ok = g < 2 || wait(raw_k_free + (g & 1), (g - 2) >> 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        issue(&P.k_map, raw_k_at + (g & 1) * C::kRawBytes, raw_k + (g & 1));
+        float2 sc = make_float2(1.0f, 0.0f);  // no row sees the slice, or it reads as zeros
+        if (wanted && in) sc = make_float2(a.k_scale[blk], a.v_scale[blk]);
+        ok = g < 1 || wait(raw_v_free, g - 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        issue(&P.v_map, raw_v_at, raw_v);
+        if (lane < 4) scales[4 * (g & 7) + lane] = sc;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(scales_full + (g & 7));
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    if (w == 0) {  // after a timeout: let the copies in flight land
-      for (; done_k < issued_k; ++done_k) tc::wait_bounded(raw_k, done_k & 1, abort_flag, P.limit_ns, a.status, true);
-      for (; done_v < issued_v; ++done_v) tc::wait_bounded(raw_v, done_v & 1, abort_flag, P.limit_ns, a.status, true);
+    if (!ok) {  // after a timeout: let the copies in flight land (one of each ring place at most is not awaited yet)
+      for (int i = 0; i < 2; ++i) {
+        const int last = g - 1 - i;
+        if (last >= 0) tc::wait_bounded(raw_k + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
+      }
+      if (g > 0) tc::wait_bounded(raw_v, (g - 1) & 1, abort_flag, P.limit_ns, a.status, true);
     }
   } else if (lane == 0) {
     // ================= the products
     const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(smem + C::kQ)), k_desc = tc::sw128_desc(tc::smem_u32(smem + C::kK));
-    const uint64_t p_desc = tc::sw128_desc(tc::smem_u32(smem + C::kP)), v_desc = tc::sw128_desc(tc::smem_u32(smem + C::kV));
-    auto product_pv = [&](int g, bool first) {
-      if (!wait(v_full, g) || !wait(p_full, g)) return false;
+    const uint64_t v_desc = tc::sw128_desc(tc::smem_u32(smem + C::kV));
+    uint32_t first_bits = 0;  // bit g & 31: block g is the first of its tile here
+    int pv = 0;               // the next block whose values are added
+    auto product_pv = [&]() {
+      const int g = pv++;
+      if (!wait(v_full + (g & 1), g >> 1) || !wait(p_full + (g & 1), g >> 1)) return false;
       tc::tc_fence_after();
+      const bool fresh = first_bits >> (g & 31) & 1;
 #pragma unroll
-      for (int k = 0; k < CH / 16; ++k)  // 16 tokens are 32 bytes of a row
-        tc::mma_dense(tmem + C::kO, p_desc + 2 * k, v_desc + 2 * k, idesc_f16(R, D), !first || k > 0);
-      tc::tc_commit(o_done);
+      for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P, 32 bytes of a row of V
+        mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + 8 * k, v_desc + (g & 1) * (CH * D * 2 / 16) + 2 * k,
+                   idesc_f16(R, D), !fresh || k > 0);
+      tc::tc_commit(o_done + (g & 1));
       return true;
     };
     int g = 0, tiles = 0;
-    bool ok = true, first_pending = false;
+    bool ok = true;
     for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G), ++tiles) {
       for (int c = cur.c; ok && c < cur.c_end; ++c, ++g) {
         const bool first = c == cur.c;
-        if (first && g > 0) ok = product_pv(g - 1, first_pending);  // the last tile's; its sums are read before Q changes
-        ok = ok && wait(k_full, g) && (g < 2 || wait(s_free + (g & 1), (g - 2) >> 1)) && (!first || wait(q_full, tiles));
+        first_bits = (first_bits & ~(1u << (g & 31))) | uint32_t(first) << (g & 31);
+        // the place of these scores was block g - 2's; at a tile's end everything is added before Q changes
+        const int upto = first ? g - 1 : g - 2;
+        while (ok && pv <= upto) ok = product_pv();
+        if (ok && upto >= 0) ok = wait(o_done + (upto & 1), upto >> 1);
+        ok = ok && wait(k_full, g) && (!first || wait(q_full, tiles));
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
@@ -562,11 +573,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           tc::mma_dense(tmem + (g & 1) * CH, q_desc + (k >> 2) * (R * 128 / 16) + 2 * (k & 3),
                         k_desc + (k >> 2) * (CH * 128 / 16) + 2 * (k & 3), idesc_f16(R, CH), k > 0);
         tc::tc_commit(s_full + (g & 1));
-        if (!first) ok = product_pv(g - 1, first_pending);
-        first_pending = first;
       }
     }
-    if (ok && g > 0) product_pv(g - 1, first_pending);
+    while (ok && pv < g) ok = product_pv();
     tc::tc_commit(drain);  // nothing in flight when the memory goes
     tc::wait_bounded(drain, 0, abort_flag, P.limit_ns, a.status, true);
   }
