@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 2);
   int* nan_block = abort_flag + 4;  // [4] 1 + number of the block whose NaN masks are valid
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 25; ++i) tc::mbar_init(bars + i, i == 11 || i == 12 || i == 15 ? 4 : 1);
+    // arrivals: of the four converting or softmax warps, or one
+    for (int i = 0; i < 25; ++i)
+      tc::mbar_init(bars + i, (i >= 2 && i <= 3) || (i >= 5 && i <= 8) || i == 11 || i == 12 || i == 15 ? 4 : 1);
     tc::fence_barrier_init();
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_block[i] = 0;
@@ -242,9 +244,11 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           scores(j0, s);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = s[16 * i];
+            float u[4];
 #pragma unroll
-            for (int j = 1; j < 16; ++j) top = fmaxf(top, s[16 * i + j]);
+            for (int j = 0; j < 4; ++j)
+              u[j] = fmaxf(fmaxf(s[16 * i + j], s[16 * i + 4 + j]), fmaxf(s[16 * i + 8 + j], s[16 * i + 12 + j]));
+            const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
             if (top != -INFINITY) mx = fmaxf(mx, top * kc[j0 / 16 + i]);
           }
         }
@@ -271,6 +275,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           }
         }
         const float base = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j0 = 0; j0 < CH; j0 += 32) {
           float s[32];
@@ -283,12 +288,13 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
             for (int j = 0; j < 8; ++j) {
               const float s0 = s[16 * i + 2 * j], s1 = s[16 * i + 2 * j + 1];
               const float p0 = ex2(fmaf(s0, k, -base)), p1 = ex2(fmaf(s1, k, -base));
-              l += p0 + p1;
+              sum[j & 3] += p0 + p1;
               w[8 * i + j] = pack_f16(p0 * vr, p1 * vr);
             }
           }
           tmem_st_16cols(s_at + j0 / 2, w);  // over scores that have been read
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
@@ -395,86 +401,96 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
     auto convert_k = [&](int g) {
       bool ok = wait(raw_k + (g & 1), g >> 1);
       if (ok && g > 0) ok = wait(s_full + ((g - 1) & 1), (g - 1) >> 1);
-      ok = tc::named_bar_and(2, 128, ok);
-      if (!ok) return false;
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
       const int tok = 32 * (w & 1) + lane;
-      const uint8_t* raw = smem + C::kRawK + (g & 1) * C::kRawBytes;
+      const uint8_t* raw = smem + C::kRawK + (g & 1) * C::kRawBytes + tok * D;
+      uint8_t* row = smem + C::kK + tok * 128;
+      uint4 x[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int p = (w >> 1) * (D / 32) + i;  // 16-byte piece of the row
-        const int at = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + at);
+        x[i] = *reinterpret_cast<const uint4*>(raw + ((p ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int p = (w >> 1) * (D / 32) + i;
         uint4 lo, hi;
-        cvt4(x.x, lo.x, lo.y);
-        cvt4(x.y, lo.z, lo.w);
-        cvt4(x.z, hi.x, hi.y);
-        cvt4(x.w, hi.z, hi.w);
-        uint8_t* dst = smem + C::kK + (p >> 2) * (CH * 128) + tok * 128;  // 64 elements a row
+        cvt4(x[i].x, lo.x, lo.y);
+        cvt4(x[i].y, lo.z, lo.w);
+        cvt4(x[i].z, hi.x, hi.y);
+        cvt4(x[i].w, hi.z, hi.w);
+        uint8_t* dst = row + (p >> 2) * (CH * 128);  // 64 elements a row
         *reinterpret_cast<uint4*>(dst + (((2 * (p & 3)) ^ (tok & 7)) << 4)) = lo;
         *reinterpret_cast<uint4*>(dst + (((2 * (p & 3) + 1) ^ (tok & 7)) << 4)) = hi;
       }
       tc::fence_proxy_async_smem();
-      tc::named_bar_sync(2, 128);
-      if (threadIdx.x == 128) {
+      __syncwarp();
+      if (lane == 0) {
         tc::mbar_arrive(k_full);
         tc::mbar_arrive(raw_k_free + (g & 1));
       }
       return true;
     };
-    // values of block g: lane = two neighbouring tokens, 16 elements of each at a time
+    // Values of block g: lane = two neighbouring tokens, 16 elements of each at a time.  A NaN must
+    // not reach the rows that do not see its token (0 x NaN): it is taken out and kept as a bit, in a
+    // mask for every token and piece; `dirty`: the places in which this thread has left bits.
+    uint32_t dirty = 0;
+    for (int i = threadIdx.x - 128; i < 4 * CH; i += 128) reinterpret_cast<uint4*>(smem + C::kNan)[i] = make_uint4(0, 0, 0, 0);
+    tc::named_bar_sync(2, 128);
     auto convert_v = [&](int g, int behind) {  // behind: tokens of the block before what no row sees
       bool ok = wait(raw_v, g);
       if (ok && g > 1) ok = wait(o_done + (g & 1), (g - 2) >> 1);
-      ok = tc::named_bar_and(2, 128, ok);
-      if (!ok) return false;
-      bool any = false;
-      uint32_t nan0[2] = {0, 0}, nan1[2] = {0, 0};
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      uint32_t x[D / 64][2][4], nan = 0;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const int p = w * (D / 64) + i;
-        uint4 x[2];
+      for (int i = 0; i < D / 64; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int tok = 2 * lane + k;
-          const int at = D == 128 ? tok * 128 + ((p ^ (tok & 7)) << 4) : tok * 64 + ((p ^ ((tok >> 1) & 3)) << 4);
-          x[k] = *reinterpret_cast<const uint4*>(smem + C::kRawV + at);
-          if (tok >= behind) x[k] = make_uint4(0, 0, 0, 0);  // anything may lie there
-        }
-        uint32_t a0[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, a1[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
-        // NaN must not reach the rows that do not see its token (0 x NaN): kept as bits, and out of the product
+          const int p = w * (D / 64) + i, tok = 2 * lane + k;
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kRawV + tok * D +
+                                                          ((p ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
+          const bool in = tok < behind;  // behind them anything may lie
+          x[i][k][0] = in ? v.x : 0, x[i][k][1] = in ? v.y : 0, x[i][k][2] = in ? v.z : 0, x[i][k][3] = in ? v.w : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t n0 = __vcmpeq4(a0[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu), n1 = __vcmpeq4(a1[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if ((n0 | n1) == 0) continue;
-          any = true;
-          a0[j] &= ~n0;
-          a1[j] &= ~n1;
-          nan0[i & 1] |= ((n0 & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * j);
-          nan1[i & 1] |= ((n1 & 0x08040201u) * 0x01010101u >> 24 & 15u) << (4 * j);
+          for (int j = 0; j < 4; ++j) nan |= (x[i][k][j] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: 0x7F, 0xFF
         }
+      if ((nan & 0x80808080u) != 0 || (dirty >> (g & 3) & 1)) {
+        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 3) * CH * 16);
+#pragma unroll 1
+        for (int i = 0; i < 2 * (D / 64); ++i) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (i == 2 * u + k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t is = ((x[u][k][j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  x[u][k][j] &= ~(is | (is - (is >> 7)));  // whole bytes
+                  bits |= ((is >> 7) * 0x01020408u >> 24 & 15u) << (4 * j);
+                }
+          mask[(2 * lane + (i & 1)) * 8 + w * (D / 64) + (i >> 1)] = uint16_t(bits);
+        }
+        const bool has = (nan & 0x80808080u) != 0;
+        dirty = (dirty & ~(1u << (g & 3))) | uint32_t(has) << (g & 3);
+        if (has) nan_block[g & 3] = g + 1;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t e[4];  // elements 4 j .. 4 j + 3 of the piece, of both tokens
-          cvt4(__byte_perm(a0[j], a1[j], 0x5140), e[0], e[1]);
-          cvt4(__byte_perm(a0[j], a1[j], 0x7362), e[2], e[3]);
-          uint8_t* dst = smem + C::kV + (g & 1) * (CH * D * 2) + (16 * p + 4 * j) * 128 + (lane & 3) * 4;
+          cvt4(__byte_perm(x[i][0][j], x[i][1][j], 0x5140), e[0], e[1]);
+          cvt4(__byte_perm(x[i][0][j], x[i][1][j], 0x7362), e[2], e[3]);
+          uint8_t* dst = smem + C::kV + (g & 1) * (CH * D * 2) + (16 * (w * (D / 64) + i) + 4 * j) * 128 + (lane & 3) * 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *reinterpret_cast<uint32_t*>(dst + k * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
         }
-      }
-      if (!tc::named_bar_and(2, 128, !any)) {
-        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 3) * CH * 16);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          mask[(2 * lane) * 8 + w * (D / 64) + i] = uint16_t(nan0[i & 1]);
-          mask[(2 * lane + 1) * 8 + w * (D / 64) + i] = uint16_t(nan1[i & 1]);
-        }
-        if (threadIdx.x == 128) nan_block[g & 3] = g + 1;
-      }
       tc::fence_proxy_async_smem();
-      tc::named_bar_sync(2, 128);
-      if (threadIdx.x == 128) {
+      __syncwarp();
+      if (lane == 0) {
         tc::mbar_arrive(v_full + (g & 1));
         tc::mbar_arrive(raw_v_free);
       }
