@@ -8,18 +8,18 @@
 // about 2 x 256 tensor-core cycles (D = 128), 512 cycles of exponentials and some
 // 700 of other softmax instructions, so the roles run side by side, and two CTAs
 // share an SM:
-//   warps 0-3   softmax, a thread per row: scores from tensor memory (read twice, for
-//               the maximum and for the probabilities: two CTAs leave 96 registers a
-//               thread), probabilities as fp16 back into the place of the scores, where
-//               the second product takes them.  The sum of the values stays in tensor
-//               memory and is rescaled only when a row's maximum grows by more than 2^8
-//               (probabilities are at most 2^8 then, well inside fp16; sums are fp32);
-//   warps 4-7   convert the e4m3 block that TMA has brought: keys as they lie, values
+//   warps 0-7   softmax, two threads per row with half of a block's scores each: scores
+//               from tensor memory, the row's maximum exchanged between the two,
+//               probabilities as fp16 back into the place of the scores, where the second
+//               product takes them.  The sum of the values stays in tensor memory and is
+//               rescaled only when a row's maximum grows by more than 2^8 (probabilities
+//               are at most 2^8 then, well inside fp16; sums are fp32);
+//   warps 8-11  convert the e4m3 block that TMA has brought: keys as they lie, values
 //               transposed (tokens in a row), both in the 128-byte swizzle that the
 //               tensor cores read;
-//   warp 8      one thread issues the products: S = Q K^T for block g into one of two
+//   warp 12     one thread issues the products: S = Q K^T for block g into one of two
 //               places once O += P V of block g - 2, which held that place, is done;
-//   warp 9      fetches: block table, scales, TMA.
+//   warp 13     fetches: block table, scales, TMA.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
 // tiles begin and end; a tile cut between CTAs is finished by the last to arrive.
 #include "attn_kv8.cuh"
@@ -39,7 +39,7 @@ struct RowsParams {
 template <int D>
 struct RowsCfg {
   static constexpr int CH = 64, R = 128;  // tokens of a block, rows of a tile
-  static constexpr int kWarps = 10, kThreads = 32 * kWarps;
+  static constexpr int kWarps = 14, kThreads = 32 * kWarps;
   static constexpr int kRawBytes = CH * D;
   static constexpr int kQ = 0;                      // [D / 64][128 rows][128 bytes], swizzled
   static constexpr int kK = kQ + R * D * 2;         // [D / 64][64 tokens][128 bytes]
@@ -49,7 +49,8 @@ struct RowsCfg {
   static constexpr int kNan = kRawV + kRawBytes;    // 4 x [64 tokens][4 words]: elements of a token that are NaN
   static constexpr int kScales = kNan + 4 * CH * 16;  // 8 x [4 slices of 16 tokens] (key, value) scales
   static constexpr int kBars = kScales + 8 * 32;
-  static constexpr int kMisc = kBars + 256;
+  static constexpr int kXch = kBars + 256;            // between a row's two threads: maxima [2][2][128], sums, query maxima
+  static constexpr int kMisc = kXch + 8 * R * 4;
   static constexpr int kSmem = kMisc + 256;
   static constexpr int kStateFloats = R * D + 2 * R;    // o (in groups of 4 columns), m, l
   static constexpr uint32_t kTmemCols = 256, kO = 128;  // S and P at 0 and 64, O from 128 on
@@ -60,18 +61,6 @@ constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
-__device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(v[0]),
-      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -110,15 +99,14 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   uint64_t *q_full = bars + 15, *drain = bars + 16;
   uint64_t* scales_full = bars + 17;                        // [8]
   float2* scales = reinterpret_cast<float2*>(smem + C::kScales);
-  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 12 words
-  int* abort_flag = reinterpret_cast<int*>(misc + 16);
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + C::kMisc);  // of make_share: 16 words
+  int* abort_flag = reinterpret_cast<int*>(misc + 20);
   int* last_flag = abort_flag + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 2);
   int* nan_block = abort_flag + 4;  // [4] 1 + number of the block whose NaN masks are valid
   if (threadIdx.x == 0) {
-    // arrivals: of the four converting or softmax warps, or one
-    for (int i = 0; i < 25; ++i)
-      tc::mbar_init(bars + i, (i >= 2 && i <= 3) || (i >= 5 && i <= 8) || i == 11 || i == 12 || i == 15 ? 4 : 1);
+    for (int i = 0; i < 25; ++i)  // arrivals: of the converting warps, of the softmax warps, or one
+      tc::mbar_init(bars + i, (i >= 2 && i <= 3) || (i >= 5 && i <= 8) ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
     tc::fence_barrier_init();
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_block[i] = 0;
@@ -128,7 +116,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Share sh;
   if (!make_share<CH, R, C::kWarps, 1>(a, G, misc, sh)) return;
-  if (warp == 8) tc::tmem_alloc(tmem_at, C::kTmemCols);
+  if (warp == 12) tc::tmem_alloc(tmem_at, C::kTmemCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -141,48 +129,58 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   cur.start<CH, R>(a, G, misc + C::kWarps, sh.u0, sh.u0 + sh.u_n);
   const int64_t v1 = sh.u0 + sh.u_n;
 
-  if (warp < 4) {
-    // ================= softmax: thread = row of the tile
-    const int row = threadIdx.x;
-    const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
+  if (warp < 8) {
+    // ================= softmax: two threads a row of the tile
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+    float* xch = reinterpret_cast<float*>(smem + C::kXch);
+    // what the row's other thread has written at the same place (both behind one barrier of the two warps)
+    auto exchange = [&](int place, float x) {
+      xch[(2 * place + half) * R + row] = x;
+      tc::named_bar_sync(3 + (warp & 3), 64);
+      return xch[(2 * place + (half ^ 1)) * R + row];
+    };
     int g = 0;
     for (; cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
       const Tile& t = cur.t;
-      // ---- this row's query, divided by a power of two, to shared memory
+      // ---- half of this row's query, divided by a power of two, to shared memory
       const int r = t.rt * R + row;
       const bool live = r < t.m * G;
-      const int64_t at = t.row0 + r / G;
-      const int head = t.h * G + r % G;
       float row_scale;
       {
-        const T* src = static_cast<const T*>(a.q) + at * a.q_ts + head * a.q_hs;
+        const T* src = static_cast<const T*>(a.q) + int64_t(t.row0 + r / G) * a.q_ts + int64_t(t.h * G + r % G) * a.q_hs +
+                       half * (D / 2);
+        uint4 raw[D / 16];
         float amax = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          float x[8];
-          if (live) {
-            load16(src + 8 * i, x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
-          }
+        for (int i = 0; i < D / 16; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (live) raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
         }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          float x[8];
+          load16(reinterpret_cast<const T*>(&raw[i]), x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        }
+        amax = fmaxf(amax, exchange(3, amax));
         const uint32_t ex = __float_as_uint(amax) >> 23;
         const bool plain = ex == 0 || ex >= 254;
         // a negative scale turns the query round, so that maxima of products are maxima of scores
         const float down = (plain ? 1.0f : __uint_as_float((254 - ex) << 23)) * (a.scale < 0.0f ? -1.0f : 1.0f);
         row_scale = (plain ? 1.0f : __uint_as_float(ex << 23)) * (fabsf(a.scale) * kLog2e);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
           float x[8];
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) {
-            load16(src + 8 * i, x);
-            v.x = pack_f16(x[0] * down, x[1] * down);
-            v.y = pack_f16(x[2] * down, x[3] * down);
-            v.z = pack_f16(x[4] * down, x[5] * down);
-            v.w = pack_f16(x[6] * down, x[7] * down);
-          }
-          *reinterpret_cast<uint4*>(smem + C::kQ + (i >> 3) * (R * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v;
+          load16(reinterpret_cast<const T*>(&raw[i]), x);
+          uint4 v;
+          v.x = pack_f16(x[0] * down, x[1] * down);
+          v.y = pack_f16(x[2] * down, x[3] * down);
+          v.z = pack_f16(x[4] * down, x[5] * down);
+          v.w = pack_f16(x[6] * down, x[7] * down);
+          const int p = half * (D / 16) + i;  // piece of 8 elements
+          *reinterpret_cast<uint4*>(smem + C::kQ + (p >> 3) * (R * 128) + row * 128 + (((p & 7) ^ (row & 7)) << 4)) = v;
         }
       }
       tc::fence_proxy_async_smem();
@@ -195,63 +193,52 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       const int last_row = min(t.m - 1, (t.rt * R + R - 1) / G);
       const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
 
-      float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;
-      uint32_t nan_row[D / 32];
+      float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;  // l: of this thread's scores
+      // elements half * D / 2 on of the row that a NaN value reaches
+      uint32_t nan_row[D / 64];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) nan_row[i] = 0;
+      for (int i = 0; i < D / 64; ++i) nan_row[i] = 0;
       // what a block's NaN values mean for this row (once the block's values have been converted)
       auto see_nan = [&](int c, int g_of) {
         if (nan_block[g_of & 3] != g_of + 1) return;
-        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kNan + (g_of & 3) * CH * 16);
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(smem + C::kNan + (g_of & 3) * CH * 16) + half * (D / 64);
         const int t0 = (t.chunk0 + c) * CH;
         for (int k = max(0, see_lo - t0); k < min(CH, see_hi - t0); ++k)
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) nan_row[i] |= mask[4 * k + i];
+          for (int i = 0; i < D / 64; ++i) nan_row[i] |= mask[4 * k + i];
       };
       bool ok = true;
       for (int c = cur.c; c < cur.c_end; ++c, ++g) {
         const bool first = c == cur.c;
         ok = wait(scales_full + (g & 7), g >> 3) && wait(s_full + (g & 1), g >> 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc::tc_fence_after();
         if (c - 2 >= cur.c) see_nan(c - 2, g - 2);  // these scores have taken the place of its probabilities
-        const int t0 = (t.chunk0 + c) * CH;
-        const bool some_hidden = t0 + CH > all_hi || t0 < all_lo;
-        const uint32_t s_at = lanes + (g & 1) * CH;
-        // 32 scores, as products; hidden ones -inf
-        auto scores = [&](int j0, float (&s)[32]) {
-          tc::tmem_ld_32cols(s_at + j0, reinterpret_cast<uint32_t(&)[32]>(s));
-          if (some_hidden) {
+        const int t0 = (t.chunk0 + c) * CH + 32 * half;  // of this thread's 32 tokens
+        float s[32];                                     // products; hidden ones -inf
+        tc::tmem_ld_32cols(lanes + (g & 1) * CH + 32 * half, reinterpret_cast<uint32_t(&)[32]>(s));
+        if (t0 + 32 > all_hi || t0 < all_lo) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (t0 + j0 + j >= see_hi || t0 + j0 + j < see_lo) s[j] = -INFINITY;
-          }
-        };
-        float kc[4], vs[4], mx = m, v_new = v_ref;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 sc = scales[4 * (g & 7) + i];
-          kc[i] = fmaxf(sc.x * row_scale, 1.0e-37f);  // not 0: hidden scores are -inf times it
-          vs[i] = sc.y;
-          v_new = fmaxf(v_new, vs[i]);
+          for (int j = 0; j < 32; ++j)
+            if (t0 + j >= see_hi || t0 + j < see_lo) s[j] = -INFINITY;
         }
+        const float4* sc = reinterpret_cast<const float4*>(scales + 4 * (g & 7));  // (key, value) scales of two slices
+        const float4 sc_mine = sc[half], sc_other = sc[half ^ 1];
+        // not 0: hidden scores are -inf times it
+        const float kc[2] = {fmaxf(sc_mine.x * row_scale, 1.0e-37f), fmaxf(sc_mine.z * row_scale, 1.0e-37f)};
+        const float v_new = fmaxf(fmaxf(v_ref, fmaxf(sc_mine.y, sc_mine.w)), fmaxf(sc_other.y, sc_other.w));
+        float mx = m;
 #pragma unroll
-        for (int j0 = 0; j0 < CH; j0 += 32) {
-          float s[32];
-          scores(j0, s);
+        for (int i = 0; i < 2; ++i) {
+          float u[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              u[j] = fmaxf(fmaxf(s[16 * i + j], s[16 * i + 4 + j]), fmaxf(s[16 * i + 8 + j], s[16 * i + 12 + j]));
-            const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-            if (top != -INFINITY) mx = fmaxf(mx, top * kc[j0 / 16 + i]);
-          }
+          for (int j = 0; j < 4; ++j)
+            u[j] = fmaxf(fmaxf(s[16 * i + j], s[16 * i + 4 + j]), fmaxf(s[16 * i + 8 + j], s[16 * i + 12 + j]));
+          const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
+          if (top != -INFINITY) mx = fmaxf(mx, top * kc[i]);
         }
+        mx = fmaxf(mx, exchange(g & 1, mx));  // two places in turn: a thread is at most one barrier ahead
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
         if (__any_sync(0xFFFFFFFFu, grow || v_new != v_ref)) {
           const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
@@ -260,40 +247,34 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
           if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
           const float fo = f * (v_ref * v_inv);
           v_ref = v_new;
-          if (!first) {  // O is this thread's once the block before has been added
+          if (!first) {  // O is these threads' once the block before has been added
             ok = __all_sync(0xFFFFFFFFu, wait(o_done + ((g - 1) & 1), (g - 1) >> 1));
             tc::tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-              uint32_t o[32];
-              tc::tmem_ld_32cols(lanes + C::kO + j, o);
+            for (int j = half * (D / 2); j < (half + 1) * (D / 2); j += 16) {
+              uint32_t o[16];
+              tc::tmem_ld_16cols(lanes + C::kO + j, o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
-              tmem_st_32cols(lanes + C::kO + j, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
+              tmem_st_16cols(lanes + C::kO + j, o);
             }
-            tc::tmem_wait_st();
           }
         }
         const float base = m == -INFINITY ? 0.0f : m;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t w[16];
 #pragma unroll
-        for (int j0 = 0; j0 < CH; j0 += 32) {
-          float s[32];
-          scores(j0, s);
-          uint32_t w[16];
+        for (int i = 0; i < 2; ++i) {
+          const float vr = (i ? sc_mine.w : sc_mine.y) * v_inv;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float k = kc[j0 / 16 + i], vr = vs[j0 / 16 + i] * v_inv;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float s0 = s[16 * i + 2 * j], s1 = s[16 * i + 2 * j + 1];
-              const float p0 = ex2(fmaf(s0, k, -base)), p1 = ex2(fmaf(s1, k, -base));
-              sum[j & 3] += p0 + p1;
-              w[8 * i + j] = pack_f16(p0 * vr, p1 * vr);
-            }
+          for (int j = 0; j < 8; ++j) {
+            const float p0 = ex2(fmaf(s[16 * i + 2 * j], kc[i], -base)), p1 = ex2(fmaf(s[16 * i + 2 * j + 1], kc[i], -base));
+            sum[j & 3] += p0 + p1;
+            w[8 * i + j] = pack_f16(p0 * vr, p1 * vr);
           }
-          tmem_st_16cols(s_at + j0 / 2, w);  // over scores that have been read
         }
+        // over scores that both threads have read: this half's probabilities take the first half's place
+        tmem_st_16cols(lanes + (g & 1) * CH + 16 * half, w);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -302,60 +283,66 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       }
       if (!ok) break;
       // ---- the tile's sums over this CTA's blocks
-      ok = wait(o_done + ((g - 1) & 1), (g - 1) >> 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      ok = __all_sync(0xFFFFFFFFu, wait(o_done + ((g - 1) & 1), (g - 1) >> 1));
+      if (!ok) break;
       tc::tc_fence_after();
       if (cur.c_end - 2 >= cur.c) see_nan(cur.c_end - 2, g - 2);
       see_nan(cur.c_end - 1, g - 1);
+      l += exchange(2, l);
       const bool whole = cur.c == 0 && cur.c_end == t.chunks;
+      const int64_t at = t.row0 + r / G;
+      const int head = t.h * G + r % G;
       float* part = P.parts + (2 * blockIdx.x + (cur.c == 0 ? 1 : 0)) * int64_t(C::kStateFloats);
       T* dst = static_cast<T*>(a.out) + at * a.o_ts + head * a.o_hs;
       auto write_lse = [&](float m_, float l_) {
-        if (a.lse && live)
+        if (a.lse && live && half == 0)
           a.lse[at * a.heads + head] = m_ == -INFINITY && l_ == 0.0f ? -INFINITY : (m_ + log2f(l_)) / kLog2e;
       };
       const float inv = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int j = 0; j < D; j += 32) {
-        uint32_t raw[32];
-        tc::tmem_ld_32cols(lanes + C::kO + j, raw);
-        float o[32];
-        uint32_t bad = 0;
+      for (int j = 0; j < D / 2; j += 16) {
+        const int d = half * (D / 2) + j;
+        uint32_t raw[16];
+        tc::tmem_ld_16cols(lanes + C::kO + d, raw);
+        float o[16];
+        uint32_t bad = nan_row[0];
+        if (D == 128 && j >= 32) bad = nan_row[D / 64 - 1];
+        bad >>= j & 31;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          if (j == 32 * i) bad = nan_row[i];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; ++k) {
           o[k] = __uint_as_float(raw[k]) * v_ref;
           if (whole) o[k] *= inv;
           if (bad >> k & 1) o[k] = __int_as_float(0x7FC00000);
         }
         if (whole) {
-          if (live)
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) store16(dst + j + k, o + k);
+          if (live) {
+            store16(dst + d, o);
+            store16(dst + d + 8, o + 8);
+          }
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(part + ((j + k) / 4 * R + row) * 4) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4*>(part + ((d + k) / 4 * R + row) * 4) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
       tc::tc_fence_before();
       if (whole) {
         write_lse(m, l);
       } else {
-        part[R * D + row] = m;
-        part[R * D + R + row] = l;
+        if (half == 0) {
+          part[R * D + row] = m;
+          part[R * D + R + row] = l;
+        }
         const int64_t unit0 = v1 - cur.left;
         const int64_t c0 = sh.owner(unit0 + kTileUnits), c1 = sh.owner(unit0 + kTileUnits + t.chunks - 1);
         __threadfence();
-        tc::named_bar_sync(1, 128);
+        tc::named_bar_sync(1, 256);
         if (threadIdx.x == 0) {
           const bool last = atomicAdd(P.counters + c0, 1u) == uint32_t(c1 - c0);
           if (last) P.counters[c0] = 0;
           *last_flag = last;
         }
-        tc::named_bar_sync(1, 128);
+        tc::named_bar_sync(1, 256);
         if (*last_flag) {  // the last to arrive joins the parts, in CTA order
           __threadfence();
           auto part_of = [&](int64_t i) { return P.parts + (2 * i + (i == c0 ? 1 : 0)) * int64_t(C::kStateFloats); };
@@ -367,16 +354,16 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
             l += __ldcg(part_of(i) + R * D + R + row) * ex2(__ldcg(part_of(i) + R * D + row) - base);
           const float inv_all = m == -INFINITY && l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-          for (int j = 0; j < D; j += 32) {
-            float o[32];
+          for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 16) {
+            float o[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+            for (int k = 0; k < 16; ++k) o[k] = 0.0f;
             for (int64_t i = c0; i <= c1; ++i) {
               const float* p = part_of(i);
               const float f = ex2(__ldcg(p + R * D + row) - base);
 #pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + ((j + k) / 4 * R + row) * 4));
+              for (int k = 0; k < 16; k += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + ((d + k) / 4 * R + row) * 4));
                 o[k] += x.x * f;
                 o[k + 1] += x.y * f;
                 o[k + 2] += x.z * f;
@@ -384,19 +371,20 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
               }
             }
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= inv_all;
-            if (live)
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) store16(dst + j + k, o + k);
+            for (int k = 0; k < 16; ++k) o[k] *= inv_all;
+            if (live) {
+              store16(dst + d, o);
+              store16(dst + d + 8, o + 8);
+            }
           }
           write_lse(m, l);
         }
-        tc::named_bar_sync(1, 128);  // the flag is read before the next cut tile writes it
+        tc::named_bar_sync(1, 256);  // the flag is read before the next cut tile writes it
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ================= conversion
-    const int w = warp - 4;
+    const int w = warp - 8;
     // keys of block g: thread = token (two threads a token, half of its elements each)
     auto convert_k = [&](int g) {
       bool ok = wait(raw_k + (g & 1), g >> 1);
@@ -435,7 +423,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
     // not reach the rows that do not see its token (0 x NaN): it is taken out and kept as a bit, in a
     // mask for every token and piece; `dirty`: the places in which this thread has left bits.
     uint32_t dirty = 0;
-    for (int i = threadIdx.x - 128; i < 4 * CH; i += 128) reinterpret_cast<uint4*>(smem + C::kNan)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x - 256; i < 4 * CH; i += 128) reinterpret_cast<uint4*>(smem + C::kNan)[i] = make_uint4(0, 0, 0, 0);
     tc::named_bar_sync(2, 128);
     auto convert_v = [&](int g, int behind) {  // behind: tokens of the block before what no row sees
       bool ok = wait(raw_v, g);
@@ -500,7 +488,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
     for (bool ok = true; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G))
       for (int c = cur.c; ok && c < cur.c_end; ++c, ++g)
         ok = convert_k(g) && convert_v(g, cur.t.hi - (cur.t.chunk0 + c) * CH);
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ================= loads: lane i < 4 has the 16-token slice i of a block
     const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
     int g = 0;
@@ -598,7 +586,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == 8) tc::tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == 12) tc::tmem_dealloc(tmem, C::kTmemCols);
 }
 
 template <typename T, int D>
