@@ -64,17 +64,18 @@ def signatures() -> dict:
 
 
 _byref = ctypes.byref
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from CPU-only builds of torch
+# the current device and stream without torch.cuda's wrappers (absent from CPU-only builds of torch)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(name: str, device: torch.device, stream, *args, tail=()):
     """Run a C entry point with `device` current: name(*args, stream, *tail)."""
     f = getattr(lib(), name)
     index = device.index
-    if torch.cuda.current_device() != index:
+    if _raw_device() != index:
         with torch.cuda.device(device):
-            s = _raw_stream(index) if stream is None else stream.cuda_stream
-            code = f(*args, s, *tail)
+            code = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream, *tail)
     else:
         code = f(*args, _raw_stream(index) if stream is None else stream.cuda_stream, *tail)
     if code:
@@ -124,8 +125,11 @@ def _heads(t: torch.Tensor, name: str, device, dtype, shape=None) -> _Heads:
     return _Heads(t.data_ptr(), t.shape[1], tok, head)
 
 
-def _like(t: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _new_heads(t: torch.Tensor) -> tuple[torch.Tensor, _Heads]:
+    """An output like t, which has been checked (its elements lie in a row)."""
+    out = torch.empty_like(t)
+    tok, head, _ = out.stride()
+    return out, _Heads(out.data_ptr(), t.shape[1], tok, head)
 
 
 def _status(status, device) -> int | None:
@@ -190,18 +194,21 @@ def patch_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     tab, n_pos, rot = _table(table, dev)
     pos = _tensor(positions, "positions", dev, torch.int32, (T,))
     if q_out is None:
-        q_out = _like(q)
-    ho = _byref(_heads(q_out, "q_out", dev, dtype, q.shape))
+        q_out, ho = _new_heads(q)
+    else:
+        ho = _heads(q_out, "q_out", dev, dtype, q.shape)
     hk = hko = None
     if k is not None:
         hk = _byref(_heads(k, "k", dev, dtype, (T, k.shape[1], D)))
         if k_out is None:
-            k_out = _like(k)
-        hko = _byref(_heads(k_out, "k_out", dev, dtype, k.shape))
+            k_out, hko = _new_heads(k)
+        else:
+            hko = _heads(k_out, "k_out", dev, dtype, k.shape)
+        hko = _byref(hko)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call("patch_rope", dev, stream, _byref(hq), hk, ho, hko, T, D, dt, pos, tab, n_pos, rot, _layout(layout),
-          1 if backward else 0, _status(status, dev))
+    _call("patch_rope", dev, stream, _byref(hq), hk, _byref(ho), hko, T, D, dt, pos, tab, n_pos, rot, _layout(layout),
+          1 if backward else 0, None if status is None else _status(status, dev))
     return q_out, k_out
 
 
@@ -303,8 +310,9 @@ def patch_attn_kv8(q: torch.Tensor, cache: KvCache8, block_table: torch.Tensor, 
     lens = _tensor(kv_lens, "kv_lens", dev, torch.int32, (batch,))
     cu = None if cu_q is None else _tensor(cu_q, "cu_q", dev, torch.int32, (batch + 1,))
     if out is None:
-        out = _like(q)
-    ho = _heads(out, "out", dev, dtype, shape)
+        out, ho = _new_heads(q)
+    else:
+        ho = _heads(out, "out", dev, dtype, shape)
     lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
     if workspace is None:
         workspace = torch.zeros(max(patch_attn_kv8_workspace_size(T, batch, H, cache), 16), dtype=torch.uint8, device=dev)
