@@ -82,7 +82,8 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // with 5 integer instructions for 8 codes: a code in the low bits of an fp16 is
 // the subnormal c 2^-24 exactly (one AND for two codes), one 4 bits higher is
 // c 2^-20, whose partner in X is stored divided by 16.  The offset 8 is taken
-// off in the accumulator, which starts at -8 2^-24 sum x of its group.
+// off in the accumulator, which starts at -8 2^-24 sum x of its group: the same
+// product with the code -8 everywhere, taken once per CTA.
 //
 // X is put in shared memory as fp16 in operand order (per 8 k: the pairs (0,4)
 // (1,5) (2,6) (3,7)), every 128 elements of a token divided by a power of two
@@ -161,11 +162,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float f16_sum(uint32_t x) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-  return f.x + f.y;
-}
-
 // S: type of the scales; NT: 8-token tiles; GS: log2 of the group.
 template <typename S, int NT, int GS>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
@@ -290,21 +286,26 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
       if (slices || chunk0 == 0) {
         __syncthreads();  // the last slice's is read
         constexpr int kAhead = 4;  // units of 8 elements a thread has under way
-        const int units = P.M * nb * 32;
-        for (int u0 = threadIdx.x; u0 < units; u0 += kAhead * C::kThreads) {
+        const int row_units = nb * 32;
+        int m = 0, at = threadIdx.x;  // token and unit of it
+        while (at >= row_units && m < P.M) at -= row_units, ++m;
+        while (m < P.M) {
           uint4 raw[kAhead];
+          int ms[kAhead], us[kAhead];
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
-            const int u = u0 + j * C::kThreads, m = u / (nb * 32), k = b0 * kBlockK + (u - m * nb * 32) * 8;
+            ms[j] = m;
+            us[j] = at;
+            const int k = b0 * kBlockK + at * 8;
             raw[j] = make_uint4(0, 0, 0, 0);
-            if (u < units && k < P.K)
+            if (m < P.M && k < P.K)
               raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.X) + int64_t(m) * P.K + k);
+            at += C::kThreads;
+            while (at >= row_units && m < P.M) at -= row_units, ++m;
           }
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
-            const int u = u0 + j * C::kThreads;
-            if (u >= units) break;  // all 16 threads of a token's 128 k together
-            const int m = u / (nb * 32), p = u & 15, half_blk = (u - m * nb * 32) >> 4;
+            if (ms[j] >= P.M) break;  // all 16 threads of a token's 128 k together
             float x[8];
             if (P.dtype == PATCH_DTYPE_BF16)
               load16(reinterpret_cast<const __nv_bfloat16*>(&raw[j]), x);
@@ -317,22 +318,28 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
 #pragma unroll
             for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
             const int e = max(int(__float_as_uint(amax) >> 23) - 127, -113);
-            const float f = e == 128 ? 1.0f : pow2i(14 - e);
-            uint4 v;
-            v.x = pack_f16(x[0] * f, x[4] * f);
-            v.y = pack_f16(x[1] * f * 0.0625f, x[5] * f * 0.0625f);
-            v.z = pack_f16(x[2] * f, x[6] * f);
-            v.w = pack_f16(x[3] * f * 0.0625f, x[7] * f * 0.0625f);
+            const float f = e == 128 ? 1.0f : pow2i(14 - e), f16 = f * 0.0625f;
             // odd tokens have the halves of 128 bytes exchanged: 8 tokens' pieces lie in different banks
-            xs[m * L.x_row + ((16 * half_blk + p) ^ ((m & 1) << 2))] = v;
-            float sum = f16_sum(v.x) + f16_sum(v.z) + 16.0f * (f16_sum(v.y) + f16_sum(v.w));
-            constexpr int kLanes = 1 << (GS - 3);  // of a group
-#pragma unroll
-            for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(half, sum, d);
-            if ((p & (kLanes - 1)) == 0)
-              neg_sum[((half_blk * 128 + 8 * p) >> GS) * 8 * NT + m] = sum * (-8.0f / 16777216.0f);
-            if (p == 0) x_scale[half_blk * 8 * NT + m] = e == 128 ? 4096.0f : pow2i(e - 2);
+            xs[ms[j] * L.x_row + (us[j] ^ ((ms[j] & 1) << 2))] =
+                make_uint4(pack_f16(x[0] * f, x[4] * f), pack_f16(x[1] * f16, x[5] * f16), pack_f16(x[2] * f, x[6] * f),
+                           pack_f16(x[3] * f16, x[7] * f16));
+            if ((threadIdx.x & 15) == 0) x_scale[(us[j] >> 4) * 8 * NT + ms[j]] = e == 128 ? 4096.0f : pow2i(e - 2);
           }
+        }
+        __syncthreads();
+        // -8 times the sums of X over each group, as the products will take them
+        for (int grp = warp; grp < nb * kGroups * NT; grp += kWarps) {
+          const int t = grp % NT, g0 = grp / NT;  // token tile, group of the slice
+          constexpr int kPer = 1 << (GS - 5);
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int c = g0 * kPer + i;
+            const uint4 x = *(t == 0 ? x_lane[0][c & 1] + c * 4 : x_lane[NT - 1][c & 1] + c * 4);
+            mma(acc, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.x, x.y, acc);
+            mma(acc, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, x.z, x.w, acc);
+          }
+          if (n == 0) *reinterpret_cast<float2*>(neg_sum + grp * 8 + 2 * q) = make_float2(acc[0], acc[1]);
         }
         __syncthreads();
       }
