@@ -591,8 +591,8 @@ static cudaError_t launch(const Params& P, int num_sms, cudaStream_t stream) {
 
 }  // namespace attn
 
-// Counters first (the same place for both kernels: up to two CTAs per SM, left zero), then two tile states per CTA.
-static size_t attn_counter_bytes(int num_sms) { return (size_t(num_sms) * 8 + 255) / 256 * 256; }
+// Counters first (the same place for both kernels, one per CTA, left zero), then two tile states per CTA.
+static size_t attn_counter_bytes(int num_sms) { return (size_t(num_sms) * 4 + 255) / 256 * 256; }
 
 // Tiles of 128 rows (attn_kv8_rows.cu) where a sequence and head have 64 query rows or more on average.
 static bool many_rows(int64_t n_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads) {
@@ -606,10 +606,10 @@ size_t attn_kv8_workspace_bytes(int64_t n_tokens, int64_t batch, int64_t q_heads
   return attn_counter_bytes(num_sms) + 2 * size_t(num_sms) * state;
 }
 
-cudaError_t launch_attn_kv8(const AttnParams& a, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
-                            int num_sms, uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_attn_kv8(const AttnParams& a, int head_dim, int dtype, void* workspace, int num_sms,
+                            uint64_t limit_ns, cudaStream_t stream) {
   if (many_rows(a.n_tokens, a.batch, a.heads, a.kv_heads))
-    return launch_attn_kv8_rows(a, head_dim, dtype, workspace, workspace_bytes, num_sms, limit_ns, stream);
+    return launch_attn_kv8_rows(a, head_dim, dtype, workspace, num_sms, limit_ns, stream);
   attn::Params P = {};
   P.a = a;
   P.counters = static_cast<uint32_t*>(workspace);

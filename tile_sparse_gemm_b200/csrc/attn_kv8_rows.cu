@@ -38,24 +38,26 @@ struct RowsParams {
 
 template <int D>
 struct RowsCfg {
-  static constexpr int CH = 64, R = 128;  // tokens of a block, rows of a tile
+  static constexpr int CH = 128, R = 128;  // tokens of a block, rows of a tile
+  static constexpr int SL = CH / 16;       // slices of 16 tokens, the least page
   static constexpr int kWarps = 14, kThreads = 32 * kWarps;
   static constexpr int kRawBytes = CH * D;
-  static constexpr int kQ = 0;                      // [D / 64][128 rows][128 bytes], swizzled
-  static constexpr int kK = kQ + R * D * 2;         // [D / 64][64 tokens][128 bytes]
-  static constexpr int kV = kK + CH * D * 2;        // 2 x [D][64 tokens]
-  static constexpr int kRawK = kV + 2 * CH * D * 2;  // 2 x e4m3 as in the cache
+  static constexpr int kQ = 0;                        // [D / 64][128 rows][128 bytes], swizzled
+  static constexpr int kK = kQ + R * D * 2;           // [D / 64][CH tokens][128 bytes]
+  static constexpr int kV = kK + CH * D * 2;          // 2 x [CH / 64][D][64 tokens]
+  static constexpr int kRawK = kV + 2 * CH * D * 2;   // 2 x e4m3 as in the cache
   static constexpr int kRawV = kRawK + 2 * kRawBytes;
-  static constexpr int kNan = kRawV + kRawBytes;    // 4 x [64 tokens][4 words]: elements of a token that are NaN
-  static constexpr int kScales = kNan + 4 * CH * 16;  // 8 x [4 slices of 16 tokens] (key, value) scales
-  static constexpr int kBars = kScales + 8 * 32;
+  static constexpr int kNan = kRawV + kRawBytes;      // 4 x [CH tokens][4 words]: elements of a token that are NaN
+  static constexpr int kScales = kNan + 4 * CH * 16;  // 8 x [SL] (key, value) scales
+  static constexpr int kBars = kScales + 8 * SL * 8;
   static constexpr int kXch = kBars + 256;            // between a row's two threads: maxima [2][2][128], sums, query maxima
   static constexpr int kMisc = kXch + 8 * R * 4;
   static constexpr int kSmem = kMisc + 256;
-  static constexpr int kStateFloats = R * D + 2 * R;    // o (in groups of 4 columns), m, l
-  static constexpr uint32_t kTmemCols = 256, kO = 128;  // S and P at 0 and 64, O from 128 on
+  static constexpr int kStateFloats = R * D + 2 * R;       // o (in groups of 4 columns), m, l
+  static constexpr uint32_t kTmemCols = 512, kO = 2 * CH;  // S and P at 0 and CH, then O
 };
 
+constexpr float kLeast = 1.0e-37f;  // of a score's factor: not 0, hidden scores are -inf times it
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
@@ -69,6 +71,11 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
+               : "memory");
+}
 // the A operand in tensor memory: lane = row, a column holds two neighbouring fp16 of k
 __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -80,9 +87,9 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
+__global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
   using C = RowsCfg<D>;
-  constexpr int CH = C::CH, R = C::R;
+  constexpr int CH = C::CH, R = C::R, SL = C::SL, kCols = CH / 2;  // kCols: scores of a block that a thread has
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnParams& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -215,28 +222,31 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
         if (!ok) break;
         tc::tc_fence_after();
         if (c - 2 >= cur.c) see_nan(c - 2, g - 2);  // these scores have taken the place of its probabilities
-        const int t0 = (t.chunk0 + c) * CH + 32 * half;  // of this thread's 32 tokens
-        float s[32];                                     // products; hidden ones -inf
-        tc::tmem_ld_32cols(lanes + (g & 1) * CH + 32 * half, reinterpret_cast<uint32_t(&)[32]>(s));
-        if (t0 + 32 > all_hi || t0 < all_lo) {
+        const int t0 = (t.chunk0 + c) * CH + kCols * half;  // of this thread's tokens
+        const uint32_t s_at = lanes + (g & 1) * CH + kCols * half;
+        float s[kCols];  // products; hidden ones -inf
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (t0 + j >= see_hi || t0 + j < see_lo) s[j] = -INFINITY;
+        for (int j = 0; j < kCols; j += 32) tc::tmem_ld_32cols(s_at + j, reinterpret_cast<uint32_t(&)[32]>(s[j]));
+        if (t0 + kCols > all_hi || t0 < all_lo) {
+          const int hi = see_hi - t0, lo = see_lo - t0;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j >= hi || j < lo) s[j] = -INFINITY;
         }
-        const float4* sc = reinterpret_cast<const float4*>(scales + 4 * (g & 7));  // (key, value) scales of two slices
-        const float4 sc_mine = sc[half], sc_other = sc[half ^ 1];
-        // not 0: hidden scores are -inf times it
-        const float kc[2] = {fmaxf(sc_mine.x * row_scale, 1.0e-37f), fmaxf(sc_mine.z * row_scale, 1.0e-37f)};
-        const float v_new = fmaxf(fmaxf(v_ref, fmaxf(sc_mine.y, sc_mine.w)), fmaxf(sc_other.y, sc_other.w));
+        const float2* sc = scales + SL * (g & 7);  // (key, value) scales of the slices
+        float v_new = v_ref;
+#pragma unroll
+        for (int i = 0; i < SL; ++i) v_new = fmaxf(v_new, sc[i].y);
+        sc += SL / 2 * half;
         float mx = m;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SL / 2; ++i) {
           float u[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             u[j] = fmaxf(fmaxf(s[16 * i + j], s[16 * i + 4 + j]), fmaxf(s[16 * i + 8 + j], s[16 * i + 12 + j]));
           const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-          if (top != -INFINITY) mx = fmaxf(mx, top * kc[i]);
+          if (top != -INFINITY) mx = fmaxf(mx, top * fmaxf(sc[i].x * row_scale, kLeast));
         }
         mx = fmaxf(mx, exchange(g & 1, mx));  // two places in turn: a thread is at most one barrier ahead
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
@@ -262,19 +272,18 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
         }
         const float base = m == -INFINITY ? 0.0f : m;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float vr = (i ? sc_mine.w : sc_mine.y) * v_inv;
+        for (int i = 0; i < SL / 2; ++i) {
+          const float k = fmaxf(sc[i].x * row_scale, kLeast), vr = sc[i].y * v_inv;
+          uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float p0 = ex2(fmaf(s[16 * i + 2 * j], kc[i], -base)), p1 = ex2(fmaf(s[16 * i + 2 * j + 1], kc[i], -base));
+            const float p0 = ex2(fmaf(s[16 * i + 2 * j], k, -base)), p1 = ex2(fmaf(s[16 * i + 2 * j + 1], k, -base));
             sum[j & 3] += p0 + p1;
-            w[8 * i + j] = pack_f16(p0 * vr, p1 * vr);
+            w[j] = pack_f16(p0 * vr, p1 * vr);
           }
+          tmem_st_8cols(s_at + 8 * i, w);  // over scores that this thread has read
         }
-        // over scores that both threads have read: this half's probabilities take the first half's place
-        tmem_st_16cols(lanes + (g & 1) * CH + 16 * half, w);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -385,31 +394,31 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
   } else if (warp < 12) {
     // ================= conversion
     const int w = warp - 8;
-    // keys of block g: thread = token (two threads a token, half of its elements each)
+    // keys of block g: thread = token
     auto convert_k = [&](int g) {
       bool ok = wait(raw_k + (g & 1), g >> 1);
       if (ok && g > 0) ok = wait(s_full + ((g - 1) & 1), (g - 1) >> 1);
       if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-      const int tok = 32 * (w & 1) + lane;
+      const int tok = 32 * w + lane;
       const uint8_t* raw = smem + C::kRawK + (g & 1) * C::kRawBytes + tok * D;
       uint8_t* row = smem + C::kK + tok * 128;
-      uint4 x[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int p = (w >> 1) * (D / 32) + i;  // 16-byte piece of the row
-        x[i] = *reinterpret_cast<const uint4*>(raw + ((p ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
-      }
+      for (int p0 = 0; p0 < D / 16; p0 += 4) {  // 16-byte pieces of the row, 64 elements of fp16 at a time
+        uint4 x[4];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int p = (w >> 1) * (D / 32) + i;
-        uint4 lo, hi;
-        cvt4(x[i].x, lo.x, lo.y);
-        cvt4(x[i].y, lo.z, lo.w);
-        cvt4(x[i].z, hi.x, hi.y);
-        cvt4(x[i].w, hi.z, hi.w);
-        uint8_t* dst = row + (p >> 2) * (CH * 128);  // 64 elements a row
-        *reinterpret_cast<uint4*>(dst + (((2 * (p & 3)) ^ (tok & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(dst + (((2 * (p & 3) + 1) ^ (tok & 7)) << 4)) = hi;
+        for (int i = 0; i < 4; ++i)
+          x[i] = *reinterpret_cast<const uint4*>(raw + (((p0 + i) ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
+        uint8_t* dst = row + (p0 >> 2) * (CH * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 lo, hi;
+          cvt4(x[i].x, lo.x, lo.y);
+          cvt4(x[i].y, lo.z, lo.w);
+          cvt4(x[i].z, hi.x, hi.y);
+          cvt4(x[i].w, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(dst + (((2 * i) ^ (tok & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((2 * i + 1) ^ (tok & 7)) << 4)) = hi;
+        }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -429,53 +438,50 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       bool ok = wait(raw_v, g);
       if (ok && g > 1) ok = wait(o_done + (g & 1), (g - 2) >> 1);
       if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-      uint32_t x[D / 64][2][4], nan = 0;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
+      uint32_t had = 0;
+#pragma unroll 2
+      for (int i = 0; i < CH / 64 * (D / 64); ++i) {
+        const int atom = i / (D / 64), p = w * (D / 64) + i % (D / 64);  // 64 tokens, 16-byte piece
+        uint32_t x[2][4], nan = 0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int p = w * (D / 64) + i, tok = 2 * lane + k;
+          const int tok = 64 * atom + 2 * lane + k;
           const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kRawV + tok * D +
                                                           ((p ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
           const bool in = tok < behind;  // behind them anything may lie
-          x[i][k][0] = in ? v.x : 0, x[i][k][1] = in ? v.y : 0, x[i][k][2] = in ? v.z : 0, x[i][k][3] = in ? v.w : 0;
+          x[k][0] = in ? v.x : 0, x[k][1] = in ? v.y : 0, x[k][2] = in ? v.z : 0, x[k][3] = in ? v.w : 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) nan |= (x[i][k][j] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: 0x7F, 0xFF
+          for (int j = 0; j < 4; ++j) nan |= (x[k][j] & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of a byte: 0x7F, 0xFF
         }
-      if ((nan & 0x80808080u) != 0 || (dirty >> (g & 3) & 1)) {
-        uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 3) * CH * 16);
-#pragma unroll 1
-        for (int i = 0; i < 2 * (D / 64); ++i) {
-          uint32_t bits = 0;
+        nan &= 0x80808080u;
+        had |= nan;
+        if (nan != 0 || (dirty >> (g & 3) & 1)) {
+          uint16_t* mask = reinterpret_cast<uint16_t*>(smem + C::kNan + (g & 3) * CH * 16) + (64 * atom + 2 * lane) * 8 + p;
 #pragma unroll
-          for (int u = 0; u < D / 64; ++u)
+          for (int k = 0; k < 2; ++k) {
+            uint32_t bits = 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (i == 2 * u + k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t is = ((x[u][k][j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                  x[u][k][j] &= ~(is | (is - (is >> 7)));  // whole bytes
-                  bits |= ((is >> 7) * 0x01020408u >> 24 & 15u) << (4 * j);
-                }
-          mask[(2 * lane + (i & 1)) * 8 + w * (D / 64) + (i >> 1)] = uint16_t(bits);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t is = ((x[k][j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              x[k][j] &= ~(is | (is - (is >> 7)));  // whole bytes
+              bits |= ((is >> 7) * 0x01020408u >> 24 & 15u) << (4 * j);
+            }
+            mask[8 * k] = uint16_t(bits);
+          }
         }
-        const bool has = (nan & 0x80808080u) != 0;
-        dirty = (dirty & ~(1u << (g & 3))) | uint32_t(has) << (g & 3);
-        if (has) nan_block[g & 3] = g + 1;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
+        uint8_t* dst = smem + C::kV + (g & 1) * (CH * D * 2) + atom * (D * 128) + 16 * p * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t e[4];  // elements 4 j .. 4 j + 3 of the piece, of both tokens
-          cvt4(__byte_perm(x[i][0][j], x[i][1][j], 0x5140), e[0], e[1]);
-          cvt4(__byte_perm(x[i][0][j], x[i][1][j], 0x7362), e[2], e[3]);
-          uint8_t* dst = smem + C::kV + (g & 1) * (CH * D * 2) + (16 * (w * (D / 64) + i) + 4 * j) * 128 + (lane & 3) * 4;
+          cvt4(__byte_perm(x[0][j], x[1][j], 0x5140), e[0], e[1]);
+          cvt4(__byte_perm(x[0][j], x[1][j], 0x7362), e[2], e[3]);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint32_t*>(dst + k * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
+            *reinterpret_cast<uint32_t*>(dst + (4 * j + k) * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
         }
+      }
+      dirty = (dirty & ~(1u << (g & 3))) | uint32_t(had != 0) << (g & 3);
+      if (had) nan_block[g & 3] = g + 1;
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -489,24 +495,24 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       for (int c = cur.c; ok && c < cur.c_end; ++c, ++g)
         ok = convert_k(g) && convert_v(g, cur.t.hi - (cur.t.chunk0 + c) * CH);
   } else if (warp == 13) {
-    // ================= loads: lane i < 4 has the 16-token slice i of a block
+    // ================= loads: lane i < SL has the 16-token slice i of a block
     const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
     int g = 0;
     bool ok = true;
     for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
       const Tile& t = cur.t;
       auto page_of = [&](int c) {
-        const int tok = (t.chunk0 + c) * CH + 16 * (lane & 3);
-        return lane < 4 && tok < t.hi ? a.block_table[t.b * a.max_pages + (tok >> P.page_shift)] : -1;
+        const int tok = (t.chunk0 + c) * CH + 16 * (lane & (SL - 1));
+        return lane < SL && tok < t.hi ? a.block_table[t.b * a.max_pages + (tok >> P.page_shift)] : -1;
       };
       int next = page_of(cur.c);
       for (int c = cur.c; c < cur.c_end; ++c, ++g) {
-        const int t0 = (t.chunk0 + c) * CH, tok = t0 + 16 * (lane & 3), phys = next;
+        const int t0 = (t.chunk0 + c) * CH, tok = t0 + 16 * (lane & (SL - 1)), phys = next;
         if (c + 1 < cur.c_end) next = page_of(c + 1);
         const int box = 1 << P.box_shift;
         const int n_box = max(min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift), 0);
         const uint32_t bytes = uint32_t(n_box * D) << P.box_shift;
-        const bool in = phys >= 0 && phys < a.n_pages, wanted = lane < 4 && tok < t.hi;
+        const bool in = phys >= 0 && phys < a.n_pages, wanted = lane < SL && tok < t.hi;
         if (wanted && !in) set_status(a.status, PATCH_DEV_BOUNDS);
         const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
         const bool leads = wanted && (16 * lane & (box - 1)) == 0;
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
         ok = g < 1 || wait(raw_v_free, g - 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.v_map, raw_v_at, raw_v);
-        if (lane < 4) scales[4 * (g & 7) + lane] = sc;
+        if (lane < SL) scales[SL * (g & 7) + lane] = sc;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(scales_full + (g & 7));
       }
@@ -553,9 +559,10 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
       tc::tc_fence_after();
       const bool fresh = first_bits >> (g & 31) & 1;
 #pragma unroll
-      for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P, 32 bytes of a row of V
-        mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + 8 * k, v_desc + (g & 1) * (CH * D * 2 / 16) + 2 * k,
-                   idesc_f16(R, D), !fresh || k > 0);
+      for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P (in its half), 32 bytes of a row of V
+        mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + kCols * (k / (SL / 2)) + 8 * (k % (SL / 2)),
+                   v_desc + (g & 1) * (CH * D * 2 / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), idesc_f16(R, D),
+                   !fresh || k > 0);
       tc::tc_commit(o_done + (g & 1));
       return true;
     };
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 2) attn_kv8_rows_kernel(
 template <typename T, int D>
 static cudaError_t launch_rows(const RowsParams& P, int ctas, cudaStream_t stream) {
   constexpr int kSmem = RowsCfg<D>::kSmem;
-  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   auto kernel = attn_kv8_rows_kernel<T, D>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
@@ -601,8 +608,8 @@ static cudaError_t launch_rows(const RowsParams& P, int ctas, cudaStream_t strea
 
 }  // namespace attn
 
-// Counters for two CTAs per SM, then the tile states of as many CTAs as there is room for, one per SM at least.
-static size_t rows_counter_bytes(int num_sms) { return (size_t(num_sms) * 8 + 255) / 256 * 256; }
+// Counters (where attn_kv8.cu has its own), then two tile states for each CTA, of which every SM has one.
+static size_t rows_counter_bytes(int num_sms) { return (size_t(num_sms) * 4 + 255) / 256 * 256; }
 static size_t rows_state_bytes(int64_t head_dim) {
   return 2 * 4 * size_t(head_dim == 128 ? attn::RowsCfg<128>::kStateFloats : attn::RowsCfg<64>::kStateFloats);
 }
@@ -610,26 +617,24 @@ size_t attn_kv8_rows_workspace_bytes(int64_t head_dim, int num_sms) {
   return rows_counter_bytes(num_sms) + num_sms * rows_state_bytes(head_dim);
 }
 
-cudaError_t launch_attn_kv8_rows(const AttnParams& a, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
+cudaError_t launch_attn_kv8_rows(const AttnParams& a, int head_dim, int dtype, void* workspace,
                                  int num_sms, uint64_t limit_ns, cudaStream_t stream) {
   attn::RowsParams P = {};
   P.a = a;
   P.counters = static_cast<uint32_t*>(workspace);
   P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + rows_counter_bytes(num_sms));
   P.limit_ns = limit_ns;
-  const int box = a.page < 64 ? a.page : 64;
+  const int box = int(a.page);  // up to a whole block
   for (P.page_shift = 4; (1 << P.page_shift) < a.page;) ++P.page_shift;
   for (P.box_shift = 4; (1 << P.box_shift) < box;) ++P.box_shift;
   if (!make_map_pages_u8(&P.k_map, a.k, head_dim, a.page, a.n_pages * a.kv_heads, box) ||
       !make_map_pages_u8(&P.v_map, a.v, head_dim, a.page, a.n_pages * a.kv_heads, box))
     return cudaErrorInvalidValue;
-  int64_t ctas = int64_t((workspace_bytes - rows_counter_bytes(num_sms)) / rows_state_bytes(head_dim));
-  if (ctas > 2 * int64_t(num_sms)) ctas = 2 * int64_t(num_sms);
   if (dtype == PATCH_DTYPE_BF16)
-    return head_dim == 128 ? attn::launch_rows<__nv_bfloat16, 128>(P, int(ctas), stream)
-                           : attn::launch_rows<__nv_bfloat16, 64>(P, int(ctas), stream);
-  return head_dim == 128 ? attn::launch_rows<__half, 128>(P, int(ctas), stream)
-                         : attn::launch_rows<__half, 64>(P, int(ctas), stream);
+    return head_dim == 128 ? attn::launch_rows<__nv_bfloat16, 128>(P, num_sms, stream)
+                           : attn::launch_rows<__nv_bfloat16, 64>(P, num_sms, stream);
+  return head_dim == 128 ? attn::launch_rows<__half, 128>(P, num_sms, stream)
+                         : attn::launch_rows<__half, 64>(P, num_sms, stream);
 }
 
 }  // namespace patch

@@ -241,7 +241,7 @@ patch_status_t patch_attn_kv8(const patch_heads* q, int64_t n_tokens, int dtype,
   P.causal = causal ? 1 : 0;
   P.scale = scale;
   const uint64_t limit_ns = (wait_limit_us ? wait_limit_us : 2000000ull) * 1000ull;
-  return launch_attn_kv8(P, int(cache->head_dim), dtype, workspace, workspace_bytes, sms, limit_ns,
+  return launch_attn_kv8(P, int(cache->head_dim), dtype, workspace, sms, limit_ns,
                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PATCH_OK
              : PATCH_ERR_CUDA;

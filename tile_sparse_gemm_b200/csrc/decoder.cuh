@@ -68,11 +68,11 @@ struct AttnParams {
 };
 size_t attn_kv8_workspace_bytes(int64_t n_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                 int num_sms);
-cudaError_t launch_attn_kv8(const AttnParams& P, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
-                            int num_sms, uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_attn_kv8(const AttnParams& P, int head_dim, int dtype, void* workspace, int num_sms,
+                            uint64_t limit_ns, cudaStream_t stream);
 // the form for many query rows per sequence and head (launch_attn_kv8 chooses)
 size_t attn_kv8_rows_workspace_bytes(int64_t head_dim, int num_sms);
-cudaError_t launch_attn_kv8_rows(const AttnParams& P, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
+cudaError_t launch_attn_kv8_rows(const AttnParams& P, int head_dim, int dtype, void* workspace,
                                  int num_sms, uint64_t limit_ns, cudaStream_t stream);
 
 cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out, int num_sms, cudaStream_t stream);
