@@ -1,4 +1,5 @@
-"""Build libpatch.so in-tree with nvcc for sm_100a (B200).
+"""Build libpatch.so in-tree with nvcc for sm_100a (B200), and the CPython
+extension of the decode step's calls beside it.
 
     python -m tile_sparse_gemm_b200.build          # compile if sources changed
     python -m tile_sparse_gemm_b200.build --force  # always recompile
@@ -10,6 +11,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -19,6 +21,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB = PKG / "libpatch.so"
 LIB_DEBUG = PKG / "libpatch_debug.so"
+BINDING = PKG / "_decoder_binding.so"
 SOURCES = ["capi.cu", "hard_mask.cu", "pack.cu", "gemm_decode.cu", "gemm_decode_tc.cu", "gemm_prefill.cu",
            "gemm_decode_noalloc.cu", "gated_mlp.cu", "gemm_decode_chain.cu", "mma_probe.cu", "validate.cu",
            "gemm64.cu", "capi_decoder.cu", "rope.cu", "kv8_append.cu", "attn_kv8.cu",
@@ -40,8 +43,32 @@ def _stale(lib: Path) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def build_binding(force: bool = False) -> Path:
+    """_decoder_binding.so: against this interpreter's and this torch's headers."""
+    import torch
+
+    src = CSRC / "decoder_binding.cpp"
+    if not force and BINDING.exists() and all(d.stat().st_mtime <= BINDING.stat().st_mtime
+                                              for d in (src, INCLUDE / "patch.h")):
+        return BINDING
+    home = Path(torch.__file__).resolve().parent
+    cuda = Path(_nvcc()).parent.parent
+    includes = [INCLUDE, home / "include", home / "include/torch/csrc/api/include", sysconfig.get_paths()["include"],
+                cuda / "include"]
+    tmp = BINDING.with_suffix(f".so.{os.getpid()}.tmp")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    *(f for i in includes for f in ("-isystem", str(i))), str(src), "-L", str(home / "lib"),
+                    "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-o", str(tmp)],
+                   check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> Path:
     lib = LIB_DEBUG if debug else LIB
+    if not debug:
+        build_binding(force)
     if not force and not _stale(lib):
         return lib
     build_dir = PKG / ("_build_debug" if debug else "_build")

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   if (!make_share<CH, R, kWarps, kWarps>(a, G, misc, sh)) return;
 
   // ---- this warp's share
-  Cursor cur;
+  Cursor cur{};
   cur.start<CH, R>(a, G, misc + kWarps + 2 * warp, sh.start(warp, kWarps), sh.start(warp + 1, kWarps));
 
   // ---- a second cursor runs ahead and fetches

@@ -8,6 +8,11 @@ that device's current stream), launch only libpatch kernels, allocate only the
 outputs they are not given, never synchronise and can be captured in a CUDA
 graph.  A device status word is optional: `status=new_status()` collects what
 the kernels report (patch_read_status).
+
+The calls of a decode step take less time on the device than their checks take
+in Python, so the ordinary ones (as documented, current device and stream) go
+through a compiled extension, csrc/decoder_binding.cpp.  It leaves every other
+call, the wrong ones among them, to the same checks here, which name the fault.
 """
 from __future__ import annotations
 
@@ -69,6 +74,21 @@ _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_binding = None
+
+
+def _fast():
+    """The compiled extension, bound to the library's entry points."""
+    global _binding
+    if _binding is None:
+        from . import _decoder_binding
+
+        _decoder_binding.bind(*(ctypes.cast(getattr(lib(), "patch_" + f), ctypes.c_void_p).value
+                                for f in ("rope", "kv8_append", "attn_kv8", "gemm4")))
+        _binding = _decoder_binding
+    return _binding
+
+
 def _call(name: str, device: torch.device, stream, *args, tail=()):
     """Run a C entry point with `device` current: name(*args, stream, *tail)."""
     f = getattr(lib(), name)
@@ -126,10 +146,10 @@ def _heads(t: torch.Tensor, name: str, device, dtype, shape=None) -> _Heads:
 
 
 def _new_heads(t: torch.Tensor) -> tuple[torch.Tensor, _Heads]:
-    """An output like t, which has been checked (its elements lie in a row)."""
-    out = torch.empty_like(t)
-    tok, head, _ = out.stride()
-    return out, _Heads(out.data_ptr(), t.shape[1], tok, head)
+    """A contiguous output of t's shape, type and device."""
+    T, H, D = t.shape
+    out = torch.empty((T, H, D), dtype=t.dtype, device=t.device)
+    return out, _Heads(out.data_ptr(), H, H * D, D)
 
 
 def _status(status, device) -> int | None:
@@ -187,6 +207,12 @@ def patch_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     backward=True turns the other way (times the table's amplitude): the
     gradient of the inputs from the gradient of the outputs.  Pass
     q_out=q, k_out=k to work in place."""
+    if stream is None:
+        r = _fast().rope(q, k, positions, table, layout, backward, q_out, k_out, status)
+        if type(r) is int and r:
+            _check(r, "patch_rope")
+        if r is not None:
+            return r
     dev, dtype = _cuda(q, "q"), q.dtype
     hq = _heads(q, "q", dev, dtype)
     dt = _dtype(q, "q", DTYPES)
@@ -265,6 +291,13 @@ def patch_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KvCache8, block_ta
     cu_new[b + 1] - 1 (int32 [batch + 1]; None: one token each) at the positions
     that follow, in the pages of block_table (int32 [batch][max_pages]).  With a
     table (patch_rope_table) the keys are rotated to their positions on the way."""
+    if stream is None:
+        r = _fast().append(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, past_lens, cu_new, table,
+                           layout, status)
+        if type(r) is int and r:
+            _check(r, "patch_kv8_append")
+        if r is not None:
+            return
     dev, dtype = _cuda(cache.k, "cache.k"), k.dtype
     c = cache.struct()
     dt = _dtype(k, "k")
@@ -299,6 +332,13 @@ def patch_attn_kv8(q: torch.Tensor, cache: KvCache8, block_table: torch.Tensor, 
     `window` of them.  A query that sees none gives zeros and lse -inf.  scale
     defaults to 1 / sqrt(D).  workspace: patch_attn_kv8_workspace_size bytes
     (uint8), zero-filled once, reusable by any later call on the same stream."""
+    if stream is None:
+        r = _fast().attn(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, kv_lens, cu_q, scale, causal, window,
+                         out, want_lse, workspace, status, wait_limit_us)
+        if type(r) is int and r:
+            _check(r, "patch_attn_kv8")
+        if r is not None:
+            return r
     dev, dtype = _cuda(cache.k, "cache.k"), q.dtype
     c = cache.struct()
     hq = _heads(q, "q", dev, dtype)
@@ -380,6 +420,12 @@ def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
 def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None,
                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X * W^T for up to 16 tokens (bf16 or fp16 [M][K]) and a 4-bit weight, fp32 sums."""
+    if stream is None:
+        r = _fast().gemm4(X, weight.codes, weight.scales, weight.group, Y, status)
+        if type(r) is int and r:
+            _check(r, "patch_gemm4")
+        if r is not None:
+            return r
     dev, dtype = _cuda(weight.codes, "codes"), X.dtype
     st = weight.struct()
     n, k = st.N, st.K
