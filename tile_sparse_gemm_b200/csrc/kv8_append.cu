@@ -11,7 +11,7 @@
 // and each output written once; the CTA takes several heads, the next one's loads
 // under way meanwhile, and reads the angles of the page's tokens once for all of
 // them.  Decode steps (a token or a few per page) are bound by latency: small CTAs,
-// one head each, that read their few tokens twice.
+// one head each, that read their tokens twice.
 #include "common.cuh"
 #include "decoder.cuh"
 #include "kernels.cuh"
@@ -257,17 +257,19 @@ __global__ void __launch_bounds__(64) kv8_append_few_kernel(const __grid_constan
 template <typename T, int D, bool kInterleaved>
 static cudaError_t launch_append(AppendParams P, int num_sms, cudaStream_t stream) {
   const int64_t items = P.cu_new ? P.n_tokens / P.page + 2 * int64_t(P.batch) : P.batch;
-  // Less than a quarter of a page per sequence: the small CTAs (64 sequences of one token, 8 heads:
-  // 3.9 us against 9.1 with a page-wide CTA).
-  if (int64_t(P.n_tokens) * 4 < int64_t(P.batch) * P.page)
+  const int units = P.page * (D / 16);  // of a full page: 64 ... 1024
+  const int64_t ctas = items * P.kv_heads * 2, at_once = int64_t(num_sms) * (1024 / units);  // 1024 threads an SM
+  // Up to half a page per sequence, and more page-wide CTAs than run at once: the small ones (8 heads of 128,
+  // page 64; 64 sequences of 1 token 3.9 us against 9.4, of 32 tokens 8.2 against 10.8, of 64 tokens 13.1
+  // against 13.9, of 128 17.3 against 14.9; one sequence of 1 token 2.7 against 2.6, of 32 tokens 5.1 against 2.9).
+  if (ctas > at_once && int64_t(P.n_tokens) * 2 <= int64_t(P.batch) * P.page)
     return launch_pdl(kv8_append_few_kernel<T, D, kInterleaved>, dim3(unsigned(items), unsigned(P.kv_heads), 2),
                       dim3(64), 0, stream, P);
-  // Several heads a CTA as long as every SM still has some.
-  const int64_t ctas = (P.n_tokens / P.page + 1) * P.kv_heads * 2;
-  P.heads_per_cta = int(ctas / (8 * int64_t(num_sms)));
-  P.heads_per_cta = P.heads_per_cta < 1 ? 1 : P.heads_per_cta > 8 ? 8 : P.heads_per_cta;
+  // Heads of a CTA: as many as let all CTAs run at once, a third or more of which find no page (two spare items
+  // a sequence).  1, 2, 4, 8 heads: 8 x 1024 tokens 22.5, 17.0, 14.5, 12.7 us; 1 x 2048 6.9, 5.2, 5.6, 8.6;
+  // 1 x 512 3.9, 4.0, 5.5, 8.5.
+  P.heads_per_cta = int(ctas >= 8 * at_once ? 8 : (ctas + at_once - 1) / at_once);
   const dim3 grid(unsigned(items), unsigned((P.kv_heads + P.heads_per_cta - 1) / P.heads_per_cta), 2);
-  const int units = P.page * (D / 16);  // of a full page: 64 ... 1024
   if (units == 64) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 64>, grid, dim3(64), 0, stream, P);
   if (units == 128) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 128>, grid, dim3(128), 0, stream, P);
   if (units == 256) return launch_pdl(kv8_append_kernel<T, D, kInterleaved, 256>, grid, dim3(256), 0, stream, P);

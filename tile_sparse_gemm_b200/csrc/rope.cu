@@ -115,9 +115,9 @@ static cudaError_t launch_rope_type(RopeParams P, int64_t n_tokens, bool interle
   if (P.heads_per_pass > heads) P.heads_per_pass = heads;
   const int passes = (heads + P.heads_per_pass - 1) / P.heads_per_pass;
   const dim3 block{unsigned(P.heads_per_pass * P.units)};
-  // Four heads a thread (8192 tokens of 64 heads of 128: 59 us with one, 45 with four) where that still leaves
-  // several CTAs per SM, else one (16 tokens of 40 heads: 1.7 us).
-  if (passes > 1 && n_tokens * ((passes + 3) / 4) >= 4 * int64_t(num_sms)) {
+  // Four heads a thread where that still leaves more than a CTA per SM, else one (40 heads of 128: 16 tokens
+  // 1.5 us with one, 1.8 with four; 128 tokens 1.8, 1.9; 256 tokens 2.4, 2.2; 2048 tokens 8.1, 6.7).
+  if (passes > 1 && n_tokens * ((passes + 3) / 4) * 2 >= 3 * int64_t(num_sms)) {
     const dim3 grid{unsigned(n_tokens), unsigned((passes + 3) / 4)};
     return launch_pdl(interleaved ? rope_kernel<T, true, 4> : rope_kernel<T, false, 4>, grid, block, 0, stream, P);
   }
