@@ -29,6 +29,8 @@
 // cache row serve directly as its operands, and values are transposed by a
 // byte permute of two tokens' words.  A page's key scale multiplies the scores,
 // its value scale (relative to the largest so far) the probabilities.
+#include <type_traits>
+
 #include "attn_kv8.cuh"
 
 namespace patch {
@@ -496,74 +498,91 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     const int d = d0 + i, j = (d % kStep) >> 1;
     return ((j * NT + (row >> 3)) * 4 + 2 * (d & 1) + (row & 1)) * 32 + 4 * (d / kStep) + ((row & 7) >> 1);
   };
-  for (int i = 0; i < 2 * kWarps;) {
-    if (!pieces[i].valid) {
-      ++i;
-      continue;
-    }
-    const Piece first = pieces[i];
-    float x[kEl], m = -INFINITY, l = 0.0f;
+  // x, m, l joined with the states that at(j) gives places of (m, l, elements from d0 on), kBatch of
+  // them under way together
+  float x[kEl], m, l;
+  auto join = [&](auto batch, int64_t count, auto at) {
+    constexpr int kBatch = decltype(batch)::value;
+    m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int k = 0; k < kEl; ++k) x[k] = 0.0f;
-    const bool comes_in = (i & 1) == 0;
-    bool ends = false;
-    do {
-      if (pieces[i].valid) {
-        const float* p = piece_at(i);
-        const float mp = p[R * D + row], lp = p[R * D + R + row];
-        const float mn = fmaxf(m, mp), base = mn == -INFINITY ? 0.0f : mn;
-        const float fa = ex2(m - base), fb = ex2(mp - base);
-        m = mn;
-        l = l * fa + lp * fb;
+    for (int64_t j0 = 0; j0 < count; j0 += kBatch) {
+      float pm[kBatch], pl[kBatch], px[kBatch][kEl];
 #pragma unroll
-        for (int k = 0; k < kEl; ++k) x[k] = x[k] * fa + p[element(k)] * fb;
-        ends = pieces[i].ends;
+      for (int j = 0; j < kBatch; ++j) {
+        pm[j] = -INFINITY, pl[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kEl; ++k) px[j][k] = 0.0f;
+        if (j0 + j < count) at(j0 + j, pm[j], pl[j], px[j]);
       }
-      ++i;
-    } while (!ends && i < 2 * kWarps && !(pieces[i].valid && (i & 1)));
+      float mn = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, pm[j]);
+      const float base = mn == -INFINITY ? 0.0f : mn, f0 = ex2(m - base);
+      m = mn;
+      l *= f0;
+#pragma unroll
+      for (int k = 0; k < kEl; ++k) x[k] *= f0;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float f = ex2(pm[j] - base);
+        l += pl[j] * f;
+#pragma unroll
+        for (int k = 0; k < kEl; ++k) x[k] += px[j][k] * f;
+      }
+    }
+  };
+  // bit 2 w + begins of what each warp has kept
+  const bool kept = lane < 2 * kWarps && pieces[lane & (2 * kWarps - 1)].valid;
+  const uint32_t valid = __ballot_sync(0xFFFFFFFFu, kept);
+  const uint32_t last = __ballot_sync(0xFFFFFFFFu, kept && pieces[lane & (2 * kWarps - 1)].ends);
+  for (uint32_t todo = valid; todo;) {
+    const int i = __ffs(todo) - 1;
+    const uint32_t from = ~0u << i, stop = last & from, begun = valid & 0xAAAAAAAAu & (from << 1);
+    int behind = stop ? __ffs(stop) : 2 * kWarps;  // of the run: its tile ends or the next one begins
+    if (begun) behind = min(behind, __ffs(begun) - 1);
+    const bool comes_in = (i & 1) == 0, ends = last >> (behind - 1) & 1;
+    uint32_t run = todo & ((1u << behind) - 1);
+    todo &= ~run;
+    const Piece first = pieces[i];
+    join(std::integral_constant<int, 4>(), __popc(run), [&](int64_t, float& pm, float& pl, float (&px)[kEl]) {
+      const float* p = piece_at(__ffs(run) - 1);
+      run &= run - 1;
+      pm = p[R * D + row];
+      pl = p[R * D + R + row];
+#pragma unroll
+      for (int k = 0; k < kEl; ++k) px[k] = p[element(k)];
+    });
     bool write = true;
     if (comes_in || !ends) {  // cut between CTAs
       const int64_t c0 = sh.owner(first.unit0 + kTileUnits), c1 = sh.owner(first.unit0 + kTileUnits + first.chunks - 1);
       float* part = P.parts + (2 * blockIdx.x + (comes_in ? 0 : 1)) * int64_t(C::kStateFloats);
 #pragma unroll
-      for (int k = 0; k < kEl; ++k) part[row * D + d0 + k] = x[k];
+      for (int k = 0; k < kEl; k += 2) *reinterpret_cast<float2*>(part + row * D + d0 + k) = make_float2(x[k], x[k + 1]);
       if (d0 == 0) {
         part[R * D + row] = m;
         part[R * D + R + row] = l;
       }
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) {
-        const bool last = atomicAdd(P.counters + c0, 1u) == uint32_t(c1 - c0);
-        if (last) P.counters[c0] = 0;
-        abort_flag[1] = last;
+      if (threadIdx.x == 0) {  // releases what the barrier has brought before it, and takes in what the others did
+        uint32_t arrived;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(P.counters + c0) : "memory");
+        if (arrived == uint32_t(c1 - c0)) P.counters[c0] = 0;
+        abort_flag[1] = arrived == uint32_t(c1 - c0);
       }
       __syncthreads();
       write = abort_flag[1] != 0;
-      if (write) {  // the last to arrive joins the parts, in CTA order
-        __threadfence();
-        const float* parts = P.parts + (2 * c0 + 1) * int64_t(C::kStateFloats);  // then 2 (c0 + 1), 2 (c0 + 2), ...
-        auto part_of = [&](int64_t c) { return c == c0 ? parts : P.parts + 2 * c * int64_t(C::kStateFloats); };
-        m = -INFINITY;
-#pragma unroll 8
-        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part_of(c) + R * D + row));
-        const float base = m == -INFINITY ? 0.0f : m;
-        l = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kEl; ++k) x[k] = 0.0f;
-#pragma unroll 4
-        for (int64_t c = c0; c <= c1; ++c) {
-          const float* p = part_of(c);
-          const float f = ex2(__ldcg(p + R * D + row) - base);
-          l += __ldcg(p + R * D + R + row) * f;
+      if (write)  // the last to arrive joins the parts, in CTA order
+        join(std::integral_constant<int, 8>(), c1 - c0 + 1, [&](int64_t j, float& pm, float& pl, float (&px)[kEl]) {
+          const float* p = P.parts + (2 * (c0 + j) + (j == 0 ? 1 : 0)) * int64_t(C::kStateFloats);
+          pm = __ldcg(p + R * D + row);
+          pl = __ldcg(p + R * D + R + row);
 #pragma unroll
           for (int k = 0; k < kEl; k += 2) {
             const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * D + d0 + k));
-            x[k] += y.x * f;
-            x[k + 1] += y.y * f;
+            px[k] = y.x, px[k + 1] = y.y;
           }
-        }
-      }
+        });
     }
     const int r = first.rt * R + row;
     if (write && r < first.m * G) {

@@ -146,7 +146,8 @@ struct Share {
 };
 
 // The whole CTA of kWarps warps.  misc: kWarps words, then for each of kStarts equal parts
-// of the share the sequence it begins in and the units before that.  false: no work for this CTA.
+// of the share the sequence it begins in and the units before that.  A share has kStarts units
+// where all together are fewer than that a CTA.  false: no work for this CTA.
 template <int CH, int R, int kWarps, int kStarts>
 __device__ __forceinline__ bool make_share(const AttnParams& a, int G, int64_t* misc, Share& s) {
   constexpr int kThreads = 32 * kWarps;
@@ -181,7 +182,7 @@ __device__ __forceinline__ bool make_share(const AttnParams& a, int G, int64_t* 
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) W += misc[w];
   }
-  const int64_t n_cta = min(int64_t(gridDim.x), W);
+  const int64_t n_cta = min(int64_t(gridDim.x), (W + kStarts - 1) / kStarts);
   if (blockIdx.x >= n_cta) return false;
   s.per = quotient(W, n_cta);
   s.more = W - s.per * n_cta;
