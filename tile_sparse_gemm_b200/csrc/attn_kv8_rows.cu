@@ -76,6 +76,37 @@ __device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&v
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
                : "memory");
 }
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // the A operand in tensor memory: lane = row, a column holds two neighbouring fp16 of k
 __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -241,11 +272,14 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         float mx = m;
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
-          float u[4];
+          const float* x = s + 16 * i;
+          float top = fmaxf(x[0], x[1]), top1 = fmaxf(x[2], x[3]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            u[j] = fmaxf(fmaxf(s[16 * i + j], s[16 * i + 4 + j]), fmaxf(s[16 * i + 8 + j], s[16 * i + 12 + j]));
-          const float top = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
+          for (int j = 4; j < 16; j += 4) {
+            top = max3(top, x[j], x[j + 1]);
+            top1 = max3(top1, x[j + 2], x[j + 3]);
+          }
+          top = fmaxf(top, top1);
           if (top != -INFINITY) mx = fmaxf(mx, top * fmaxf(sc[i].x * row_scale, kLeast));
         }
         mx = fmaxf(mx, exchange(g & 1, mx));  // two places in turn: a thread is at most one barrier ahead
@@ -271,20 +305,25 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
           }
         }
         const float base = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t base2 = pack2(-base, -base);
+        uint64_t sum[2] = {0, 0};  // of even and odd scores, in turn
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
           const float k = fmaxf(sc[i].x * row_scale, kLeast), vr = sc[i].y * v_inv;
+          const uint64_t k2 = pack2(k, k), vr2 = pack2(vr, vr);
           uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float p0 = ex2(fmaf(s[16 * i + 2 * j], k, -base)), p1 = ex2(fmaf(s[16 * i + 2 * j + 1], k, -base));
-            sum[j & 3] += p0 + p1;
-            w[j] = pack_f16(p0 * vr, p1 * vr);
+            const float2 e = unpack2(fma2(pack2(s[16 * i + 2 * j], s[16 * i + 2 * j + 1]), k2, base2));
+            const uint64_t p = pack2(ex2(e.x), ex2(e.y));
+            sum[j & 1] = add2(sum[j & 1], p);
+            const float2 weight = unpack2(mul2(p, vr2));
+            w[j] = pack_f16(weight.x, weight.y);
           }
           tmem_st_8cols(s_at + 8 * i, w);  // over scores that this thread has read
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 both = unpack2(add2(sum[0], sum[1]));
+        l += both.x + both.y;
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
@@ -344,16 +383,15 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         }
         const int64_t unit0 = v1 - cur.left;
         const int64_t c0 = sh.owner(unit0 + kTileUnits), c1 = sh.owner(unit0 + kTileUnits + t.chunks - 1);
-        __threadfence();
         tc::named_bar_sync(1, 256);
-        if (threadIdx.x == 0) {
-          const bool last = atomicAdd(P.counters + c0, 1u) == uint32_t(c1 - c0);
-          if (last) P.counters[c0] = 0;
-          *last_flag = last;
+        if (threadIdx.x == 0) {  // releases what the barrier has brought before it, and takes in what the others did
+          uint32_t arrived;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(arrived) : "l"(P.counters + c0) : "memory");
+          if (arrived == uint32_t(c1 - c0)) P.counters[c0] = 0;
+          *last_flag = arrived == uint32_t(c1 - c0);
         }
         tc::named_bar_sync(1, 256);
         if (*last_flag) {  // the last to arrive joins the parts, in CTA order
-          __threadfence();
           auto part_of = [&](int64_t i) { return P.parts + (2 * i + (i == c0 ? 1 : 0)) * int64_t(C::kStateFloats); };
           m = -INFINITY;
           for (int64_t i = c0; i <= c1; ++i) m = fmaxf(m, __ldcg(part_of(i) + R * D + row));
