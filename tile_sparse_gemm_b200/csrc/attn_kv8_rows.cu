@@ -76,6 +76,24 @@ __device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&v
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld_64cols(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+      "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+      "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+      "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+      "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]),
+      "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]), "=r"(v[42]),
+      "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
+      "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
+      "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t r;
@@ -142,6 +160,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
   int* last_flag = abort_flag + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 2);
   int* nan_block = abort_flag + 4;  // [4] 1 + number of the block whose NaN masks are valid
+  float* v_max = reinterpret_cast<float*>(misc + 24);  // [8] the largest value scale of a block
   if (threadIdx.x == 0) {
     for (int i = 0; i < 25; ++i)  // arrivals: of the converting warps, of the softmax warps, or one
       tc::mbar_init(bars + i, (i >= 2 && i <= 3) || (i >= 5 && i <= 8) ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
@@ -245,42 +264,42 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) nan_row[i] |= mask[4 * k + i];
       };
-      bool ok = true;
+      // A wait that runs out does not end the loops: what follows is of no use then, but every warp still
+      // goes through the barriers that it shares with others.
       for (int c = cur.c; c < cur.c_end; ++c, ++g) {
         const bool first = c == cur.c;
-        ok = wait(scales_full + (g & 7), g >> 3) && wait(s_full + (g & 1), g >> 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        wait(scales_full + (g & 7), g >> 3);
+        wait(s_full + (g & 1), g >> 1);
+        __syncwarp();
         tc::tc_fence_after();
         if (c - 2 >= cur.c) see_nan(c - 2, g - 2);  // these scores have taken the place of its probabilities
         const int t0 = (t.chunk0 + c) * CH + kCols * half;  // of this thread's tokens
         const uint32_t s_at = lanes + (g & 1) * CH + kCols * half;
-        float s[kCols];  // products; hidden ones -inf
+        // the slices' key scales (times the row's) and value scales, read before the scores so that their latency is hidden
+        float kf[SL / 2], vs[SL / 2];
 #pragma unroll
-        for (int j = 0; j < kCols; j += 32) tc::tmem_ld_32cols(s_at + j, reinterpret_cast<uint32_t(&)[32]>(s[j]));
+        for (int i = 0; i < SL / 2; i += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(scales + SL * (g & 7) + SL / 2 * half + i);
+          kf[i] = fmaxf(x.x * row_scale, kLeast), vs[i] = x.y;
+          kf[i + 1] = fmaxf(x.z * row_scale, kLeast), vs[i + 1] = x.w;
+        }
+        const float v_new = fmaxf(v_ref, v_max[g & 7]);
+        float s[kCols];  // products; hidden ones -inf
+        tmem_ld_64cols(s_at, reinterpret_cast<uint32_t(&)[64]>(s));
         if (t0 + kCols > all_hi || t0 < all_lo) {
           const int hi = see_hi - t0, lo = see_lo - t0;
 #pragma unroll
           for (int j = 0; j < kCols; ++j)
             if (j >= hi || j < lo) s[j] = -INFINITY;
         }
-        const float2* sc = scales + SL * (g & 7);  // (key, value) scales of the slices
-        float v_new = v_ref;
-#pragma unroll
-        for (int i = 0; i < SL; ++i) v_new = fmaxf(v_new, sc[i].y);
-        sc += SL / 2 * half;
         float mx = m;
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
           const float* x = s + 16 * i;
-          float top = fmaxf(x[0], x[1]), top1 = fmaxf(x[2], x[3]);
+          float top[4];
 #pragma unroll
-          for (int j = 4; j < 16; j += 4) {
-            top = max3(top, x[j], x[j + 1]);
-            top1 = max3(top1, x[j + 2], x[j + 3]);
-          }
-          top = fmaxf(top, top1);
-          if (top != -INFINITY) mx = fmaxf(mx, top * fmaxf(sc[i].x * row_scale, kLeast));
+          for (int j = 0; j < 4; ++j) top[j] = max3(x[4 * j], x[4 * j + 1], fmaxf(x[4 * j + 2], x[4 * j + 3]));
+          mx = fmaxf(mx, fmaxf(max3(top[0], top[1], top[2]), top[3]) * kf[i]);
         }
         mx = fmaxf(mx, exchange(g & 1, mx));  // two places in turn: a thread is at most one barrier ahead
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
@@ -292,7 +311,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
           const float fo = f * (v_ref * v_inv);
           v_ref = v_new;
           if (!first) {  // O is these threads' once the block before has been added
-            ok = __all_sync(0xFFFFFFFFu, wait(o_done + ((g - 1) & 1), (g - 1) >> 1));
+            wait(o_done + ((g - 1) & 1), (g - 1) >> 1);
+            __syncwarp();
             tc::tc_fence_after();
 #pragma unroll 1
             for (int j = half * (D / 2); j < (half + 1) * (D / 2); j += 16) {
@@ -309,8 +329,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         uint64_t sum[2] = {0, 0};  // of even and odd scores, in turn
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
-          const float k = fmaxf(sc[i].x * row_scale, kLeast), vr = sc[i].y * v_inv;
-          const uint64_t k2 = pack2(k, k), vr2 = pack2(vr, vr);
+          const float vr = vs[i] * v_inv;
+          const uint64_t k2 = pack2(kf[i], kf[i]), vr2 = pack2(vr, vr);
           uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -329,10 +349,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + (g & 1));
       }
-      if (!ok) break;
       // ---- the tile's sums over this CTA's blocks
-      ok = __all_sync(0xFFFFFFFFu, wait(o_done + ((g - 1) & 1), (g - 1) >> 1));
-      if (!ok) break;
+      wait(o_done + ((g - 1) & 1), (g - 1) >> 1);
+      __syncwarp();
       tc::tc_fence_after();
       if (cur.c_end - 2 >= cur.c) see_nan(cur.c_end - 2, g - 2);
       see_nan(cur.c_end - 1, g - 1);
@@ -573,6 +592,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.v_map, raw_v_at, raw_v);
         if (lane < SL) scales[SL * (g & 7) + lane] = sc;
+        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sc.y));  // none is negative
+        if (lane == 0) v_max[g & 7] = __uint_as_float(most);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(scales_full + (g & 7));
       }
