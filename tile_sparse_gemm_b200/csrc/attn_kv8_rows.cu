@@ -22,6 +22,8 @@
 //   warp 13     fetches: block table, scales, TMA.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
 // tiles begin and end; a tile cut between CTAs is finished by the last to arrive.
+#include <type_traits>
+
 #include "attn_kv8.cuh"
 
 namespace patch {
@@ -36,15 +38,15 @@ struct RowsParams {
   int page_shift, box_shift;
 };
 
-template <int D>
+// TERMS: e4m3 numbers whose sum stands for a query element.
+template <int D, int N_TERMS>
 struct RowsCfg {
-  static constexpr int CH = 128, R = 128;  // tokens of a block, rows of a tile
+  static constexpr int TERMS = N_TERMS, CH = 128, R = 128;  // tokens of a block, rows of a tile
   static constexpr int SL = CH / 16;       // slices of 16 tokens, the least page
   static constexpr int kWarps = 14, kThreads = 32 * kWarps;
   static constexpr int kRawBytes = CH * D;
-  static constexpr int kQ = 0;                        // [D / 64][128 rows][128 bytes], swizzled
-  static constexpr int kK = kQ + R * D * 2;           // [D / 64][CH tokens][128 bytes]
-  static constexpr int kV = kK + CH * D * 2;          // 2 x [CH / 64][D][64 tokens]
+  static constexpr int kQ = 0;                        // [TERMS][128 rows][D bytes], swizzled like the cache's
+  static constexpr int kV = kQ + TERMS * R * D;       // 2 x [CH / 64][D][64 tokens]
   static constexpr int kRawK = kV + 2 * CH * D * 2;   // 2 x e4m3 as in the cache
   static constexpr int kRawV = kRawK + 2 * kRawBytes;
   static constexpr int kNan = kRawV + kRawBytes;      // 4 x [CH tokens][4 words]: elements of a token that are NaN
@@ -60,7 +62,8 @@ struct RowsCfg {
 constexpr float kLeast = 1.0e-37f;  // of a score's factor: not 0, hidden scores are -inf times it
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
 
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+// fp32 sums of fp16 (kind::f16) or of e4m3 (kind::f8f6f4): type codes 0 both
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
   return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -126,6 +129,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // the A operand in tensor memory: lane = row, a column holds two neighbouring fp16 of k
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {  // saturating, NaN stays NaN
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
@@ -136,9 +152,12 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
-  using C = RowsCfg<D>;
-  constexpr int CH = C::CH, R = C::R, SL = C::SL, kCols = CH / 2;  // kCols: scores of a block that a thread has
+using RowsOf = RowsCfg<D, std::is_same<T, __half>::value ? 3 : 2>;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kernel(const __grid_constant__ RowsParams P) {
+  using C = RowsOf<T, D>;
+  constexpr int CH = C::CH, R = C::R, SL = C::SL, TERMS = C::TERMS, kCols = CH / 2;  // kCols: scores of a block that a thread has
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnParams& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,10 +165,10 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
   // Barriers of the pipeline.  Those with two or more places take blocks in turn, so that no
   // waiter is ever two phases behind.
-  uint64_t *raw_k = bars, *raw_k_free = bars + 2;           // [2] key bytes landed, read
+  uint64_t* raw_k = bars;                                   // [2] key bytes landed
   uint64_t *raw_v = bars + 4, *raw_v_free = bars + 5;       // value bytes landed, read
-  uint64_t *k_full = bars + 6, *v_full = bars + 7;          // converted; values [2]
-  uint64_t* s_full = bars + 9;                              // [2] scores done (the keys may be written again)
+  uint64_t* v_full = bars + 7;                              // [2] values converted
+  uint64_t* s_full = bars + 9;                              // [2] scores done (the keys' place is free)
   uint64_t* p_full = bars + 11;                             // [2] probabilities written
   uint64_t* o_done = bars + 13;                             // [2] O += P V done
   uint64_t *q_full = bars + 15, *drain = bars + 16;
@@ -163,7 +182,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
   float* v_max = reinterpret_cast<float*>(misc + 24);  // [8] the largest value scale of a block
   if (threadIdx.x == 0) {
     for (int i = 0; i < 25; ++i)  // arrivals: of the converting warps, of the softmax warps, or one
-      tc::mbar_init(bars + i, (i >= 2 && i <= 3) || (i >= 5 && i <= 8) ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
+      tc::mbar_init(bars + i, i == 5 || i == 7 || i == 8 ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
     tc::fence_barrier_init();
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_block[i] = 0;
@@ -222,22 +241,37 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
           for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
         }
         amax = fmaxf(amax, exchange(3, amax));
-        const uint32_t ex = __float_as_uint(amax) >> 23;
-        const bool plain = ex == 0 || ex >= 254;
+        // the largest to [2^7, 2^8); an infinity becomes NaN, which all its scores would be
+        const int e = min(134 - int(__float_as_uint(amax) >> 23), 126);
         // a negative scale turns the query round, so that maxima of products are maxima of scores
-        const float down = (plain ? 1.0f : __uint_as_float((254 - ex) << 23)) * (a.scale < 0.0f ? -1.0f : 1.0f);
-        row_scale = (plain ? 1.0f : __uint_as_float(ex << 23)) * (fabsf(a.scale) * kLog2e);
+        const float down = pow2i(e) * (a.scale < 0.0f ? -1.0f : 1.0f);
+        row_scale = pow2i(-e) * (fabsf(a.scale) * kLog2e);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          float x[8];
-          load16(reinterpret_cast<const T*>(&raw[i]), x);
-          uint4 v;
-          v.x = pack_f16(x[0] * down, x[1] * down);
-          v.y = pack_f16(x[2] * down, x[3] * down);
-          v.z = pack_f16(x[4] * down, x[5] * down);
-          v.w = pack_f16(x[6] * down, x[7] * down);
-          const int p = half * (D / 16) + i;  // piece of 8 elements
-          *reinterpret_cast<uint4*>(smem + C::kQ + (p >> 3) * (R * 128) + row * 128 + (((p & 7) ^ (row & 7)) << 4)) = v;
+        for (int i = 0; i < D / 32; ++i) {  // pieces of 16 elements
+          float x[16];
+          load16(reinterpret_cast<const T*>(&raw[2 * i]), x);
+          load16(reinterpret_cast<const T*>(&raw[2 * i + 1]), x + 8);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = amax < INFINITY ? x[j] * down : __int_as_float(0x7FC00000);
+          const int p = half * (D / 32) + i;
+          uint8_t* dst = smem + C::kQ + row * D + ((p ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = pack_e4m3(x[4 * j], x[4 * j + 1]) | pack_e4m3(x[4 * j + 2], x[4 * j + 3]) << 16;
+              uint32_t taken[2];
+              cvt4(w[j], taken[0], taken[1]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {  // what is left, exactly
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&taken[k]));
+                x[4 * j + 2 * k] -= y.x;
+                x[4 * j + 2 * k + 1] -= y.y;
+              }
+            }
+            *reinterpret_cast<uint4*>(dst + term * (R * D)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
       tc::fence_proxy_async_smem();
@@ -449,42 +483,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
       }
     }
   } else if (warp < 12) {
-    // ================= conversion
+    // ================= conversion of values
     const int w = warp - 8;
-    // keys of block g: thread = token
-    auto convert_k = [&](int g) {
-      bool ok = wait(raw_k + (g & 1), g >> 1);
-      if (ok && g > 0) ok = wait(s_full + ((g - 1) & 1), (g - 1) >> 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-      const int tok = 32 * w + lane;
-      const uint8_t* raw = smem + C::kRawK + (g & 1) * C::kRawBytes + tok * D;
-      uint8_t* row = smem + C::kK + tok * 128;
-#pragma unroll
-      for (int p0 = 0; p0 < D / 16; p0 += 4) {  // 16-byte pieces of the row, 64 elements of fp16 at a time
-        uint4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = *reinterpret_cast<const uint4*>(raw + (((p0 + i) ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
-        uint8_t* dst = row + (p0 >> 2) * (CH * 128);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 lo, hi;
-          cvt4(x[i].x, lo.x, lo.y);
-          cvt4(x[i].y, lo.z, lo.w);
-          cvt4(x[i].z, hi.x, hi.y);
-          cvt4(x[i].w, hi.z, hi.w);
-          *reinterpret_cast<uint4*>(dst + (((2 * i) ^ (tok & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((2 * i + 1) ^ (tok & 7)) << 4)) = hi;
-        }
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(k_full);
-        tc::mbar_arrive(raw_k_free + (g & 1));
-      }
-      return true;
-    };
     // Values of block g: lane = two neighbouring tokens, 16 elements of each at a time.  A NaN must
     // not reach the rows that do not see its token (0 x NaN): it is taken out and kept as a bit, in a
     // mask for every token and piece; `dirty`: the places in which this thread has left bits.
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
     int g = 0;
     for (bool ok = true; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G))
       for (int c = cur.c; ok && c < cur.c_end; ++c, ++g)
-        ok = convert_k(g) && convert_v(g, cur.t.hi - (cur.t.chunk0 + c) * CH);
+        ok = convert_v(g, cur.t.hi - (cur.t.chunk0 + c) * CH);
   } else if (warp == 13) {
     // ================= loads: lane i < SL has the 16-token slice i of a block
     const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
           __syncwarp();
           if (leads) tma_load_3d(dst + 16 * lane * D, map, tc::smem_u32(bar), 0, tok & (a.page - 1), blk);
         };
-        ok = g < 2 || wait(raw_k_free + (g & 1), (g - 2) >> 1);
+        ok = g < 2 || wait(s_full + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.k_map, raw_k_at + (g & 1) * C::kRawBytes, raw_k + (g & 1));
         float2 sc = make_float2(1.0f, 0.0f);  // no row sees the slice, or it reads as zeros
@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
     }
   } else if (lane == 0) {
     // ================= the products
-    const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(smem + C::kQ)), k_desc = tc::sw128_desc(tc::smem_u32(smem + C::kK));
+    const uint32_t q_at = tc::smem_u32(smem + C::kQ), k_at = tc::smem_u32(smem + C::kRawK);
+    const uint64_t q_desc = D == 128 ? tc::sw128_desc(q_at) : tc::sw64_desc(q_at);
+    const uint64_t k_desc = D == 128 ? tc::sw128_desc(k_at) : tc::sw64_desc(k_at);
     const uint64_t v_desc = tc::sw128_desc(tc::smem_u32(smem + C::kV));
     uint32_t first_bits = 0;  // bit g & 31: block g is the first of its tile here
     int pv = 0;               // the next block whose values are added
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
 #pragma unroll
       for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P (in its half), 32 bytes of a row of V
         mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + kCols * (k / (SL / 2)) + 8 * (k % (SL / 2)),
-                   v_desc + (g & 1) * (CH * D * 2 / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), idesc_f16(R, D),
+                   v_desc + (g & 1) * (CH * D * 2 / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), idesc_f32(R, D),
                    !fresh || k > 0);
       tc::tc_commit(o_done + (g & 1));
       return true;
@@ -635,13 +637,13 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
         const int upto = first ? g - 1 : g - 2;
         while (ok && pv <= upto) ok = product_pv();
         if (ok && upto >= 0) ok = wait(o_done + (upto & 1), upto >> 1);
-        ok = ok && wait(k_full, g) && (!first || wait(q_full, tiles));
+        ok = ok && wait(raw_k + (g & 1), g >> 1) && (!first || wait(q_full, tiles));
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_dense(tmem + (g & 1) * CH, q_desc + (k >> 2) * (R * 128 / 16) + 2 * (k & 3),
-                        k_desc + (k >> 2) * (CH * 128 / 16) + 2 * (k & 3), idesc_f16(R, CH), k > 0);
+        for (int k = 0; k < TERMS * (D / 32); ++k)  // 32 bytes of a row at a time, term after term
+          mma_e4m3(tmem + (g & 1) * CH, q_desc + (k / (D / 32)) * (R * D / 16) + 2 * (k % (D / 32)),
+                   k_desc + (g & 1) * (C::kRawBytes / 16) + 2 * (k % (D / 32)), idesc_f32(R, CH), k > 0);
         tc::tc_commit(s_full + (g & 1));
       }
     }
@@ -657,12 +659,13 @@ __global__ void __launch_bounds__(RowsCfg<D>::kThreads, 1) attn_kv8_rows_kernel(
 
 template <typename T, int D>
 static cudaError_t launch_rows(const RowsParams& P, int ctas, cudaStream_t stream) {
-  constexpr int kSmem = RowsCfg<D>::kSmem;
+  using C = RowsOf<T, D>;
+  constexpr int kSmem = C::kSmem;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   auto kernel = attn_kv8_rows_kernel<T, D>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(unsigned(ctas)), dim3(RowsCfg<D>::kThreads), kSmem, stream, P);
+  return launch_pdl(kernel, dim3(unsigned(ctas)), dim3(C::kThreads), kSmem, stream, P);
 }
 
 }  // namespace attn
@@ -670,7 +673,7 @@ static cudaError_t launch_rows(const RowsParams& P, int ctas, cudaStream_t strea
 // Counters (where attn_kv8.cu has its own), then two tile states for each CTA, of which every SM has one.
 static size_t rows_counter_bytes(int num_sms) { return (size_t(num_sms) * 4 + 255) / 256 * 256; }
 static size_t rows_state_bytes(int64_t head_dim) {
-  return 2 * 4 * size_t(head_dim == 128 ? attn::RowsCfg<128>::kStateFloats : attn::RowsCfg<64>::kStateFloats);
+  return 2 * 4 * size_t(head_dim == 128 ? attn::RowsCfg<128, 2>::kStateFloats : attn::RowsCfg<64, 2>::kStateFloats);
 }
 size_t attn_kv8_rows_workspace_bytes(int64_t head_dim, int num_sms) {
   return rows_counter_bytes(num_sms) + num_sms * rows_state_bytes(head_dim);
