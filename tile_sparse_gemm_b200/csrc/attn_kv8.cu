@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     });
     bool write = true;
     if (comes_in || !ends) {  // cut between CTAs
-      const int64_t c0 = sh.owner(first.unit0 + kTileUnits), c1 = sh.owner(first.unit0 + kTileUnits + first.chunks - 1);
+      const int64_t c0 = sh.owner(first.unit0 + tile_units<R>()), c1 = sh.owner(first.unit0 + tile_units<R>() + first.chunks - 1);
       float* part = P.parts + (2 * blockIdx.x + (comes_in ? 0 : 1)) * int64_t(C::kStateFloats);
 #pragma unroll
       for (int k = 0; k < kEl; k += 2) *reinterpret_cast<float2*>(part + row * D + d0 + k) = make_float2(x[k], x[k + 1]);

@@ -73,9 +73,13 @@ __device__ __forceinline__ int row_tiles(int m, int G) {
   return (m * G + R - 1) / R;
 }
 
-// Shares are equal in units: a chunk is one, and a tile's own cost (its queries,
-// its output; about half a chunk's time in a warp) is kTileUnits in front of its chunks.
-constexpr int kTileUnits = 1;
+// Shares are equal in units: a chunk is one, and a tile's own cost (its queries, its output) is
+// tile_units in front of its chunks: about half a chunk's time in a warp with 8 or 16 rows, 8000
+// cycles against a block's 2600 with 128 (chunks of four prompts: 206 us with one unit, 196 with three).
+template <int R>
+constexpr int tile_units() {
+  return R == 128 ? 4 : 1;
+}
 
 // units of all of a sequence's tiles of one head
 template <int CH, int R>
@@ -85,12 +89,12 @@ __device__ __forceinline__ int64_t units_per_head(const AttnParams& a, int G, Ti
   if (!a.causal) {
     t.rt = 0;
     set_rows<CH, R>(a, G, t);
-    return int64_t(n) * (t.chunks + kTileUnits);
+    return int64_t(n) * (t.chunks + tile_units<R>());
   }
   int64_t s = 0;
   for (t.rt = 0; t.rt < n; ++t.rt) {
     set_rows<CH, R>(a, G, t);
-    s += t.chunks + kTileUnits;
+    s += t.chunks + tile_units<R>();
   }
   return s;
 }
@@ -117,17 +121,20 @@ struct Cursor {
   int c, c_end;
   int64_t left;
 
-  __device__ __forceinline__ void clip() { c_end = int(min(int64_t(t.chunks), max(left - kTileUnits, int64_t(0)))); }
+  template <int R>
+  __device__ __forceinline__ void clip() {
+    c_end = int(min(int64_t(t.chunks), max(left - tile_units<R>(), int64_t(0))));
+  }
   // The part [v0, v1) of all units; at: the sequence that v0 lies in and the units before it (make_share).
   template <int CH, int R>
   __device__ __forceinline__ void start(const AttnParams& a, int G, const int64_t* at, int64_t v0, int64_t v1);
   template <int CH, int R>
   __device__ __forceinline__ void next(const AttnParams& a, int G) {
-    left -= t.chunks + kTileUnits;
+    left -= t.chunks + tile_units<R>();
     c = c_end = 0;
-    if (left <= kTileUnits) return;
+    if (left <= tile_units<R>()) return;
     next_tile<CH, R>(a, G, t);
-    clip();
+    clip<R>();
   }
 };
 
@@ -227,14 +234,14 @@ __device__ __forceinline__ void Cursor::start(const AttnParams& a, int G, const 
   off -= per_head * t.h;
   t.rt = 0;
   set_rows<CH, R>(a, G, t);
-  while (off >= t.chunks + kTileUnits) {
-    off -= t.chunks + kTileUnits;
+  while (off >= t.chunks + tile_units<R>()) {
+    off -= t.chunks + tile_units<R>();
     ++t.rt;
     set_rows<CH, R>(a, G, t);
   }
   left = v1 - (v0 - off);
-  c = int(max(off - kTileUnits, int64_t(0)));
-  clip();
+  c = int(max(off - tile_units<R>(), int64_t(0)));
+  clip<R>();
 }
 
 }  // namespace attn

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
           part[R * D + R + row] = l;
         }
         const int64_t unit0 = v1 - cur.left;
-        const int64_t c0 = sh.owner(unit0 + kTileUnits), c1 = sh.owner(unit0 + kTileUnits + t.chunks - 1);
+        const int64_t c0 = sh.owner(unit0 + tile_units<R>()), c1 = sh.owner(unit0 + tile_units<R>() + t.chunks - 1);
         tc::named_bar_sync(1, 256);
         if (threadIdx.x == 0) {  // releases what the barrier has brought before it, and takes in what the others did
           uint32_t arrived;
