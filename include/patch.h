@@ -771,7 +771,8 @@ PATCH_API patch_status_t patch_rope_table(int64_t n_pos, int64_t rot_dim, const 
  * dev_status may be NULL.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts of input and output that
  * differ, unknown layout or dtype), PATCH_ERR_SHAPE (rot_dim not a multiple of 16 in
- * 16 .. head_dim, head_dim not a multiple of 8 up to 1024, n_tokens > 2^30), PATCH_ERR_ALIGN,
+ * 16 .. head_dim, head_dim not a multiple of 8 up to 1024, n_tokens or n_pos > 2^30, more than
+ * 65535 heads of q and k together), PATCH_ERR_ALIGN,
  * PATCH_ERR_DEVICE, PATCH_ERR_CUDA.  n_tokens == 0 is a no-op.
  */
 #define PATCH_ROPE_HALF 0
@@ -817,8 +818,9 @@ typedef struct {
  * position lies outside the table, sets PATCH_DEV_BOUNDS; its page is not
  * written.  dev_status may be NULL.  Two sequences must not append to one page.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts, dtype, layout, n_tokens != batch
- * without cu_new), PATCH_ERR_SHAPE (page, head_dim, rot_dim not a multiple of 16 up to head_dim,
- * counts out of range), PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ * without cu_new), PATCH_ERR_SHAPE (page, head_dim, rot_dim not a multiple of 16 up to head_dim;
+ * kv_heads > 65535, n_pages * kv_heads >= 2^31, n_tokens, max_pages or n_pos > 2^30, batch > 2^28),
+ * PATCH_ERR_ALIGN, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
  */
 PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_heads *v, int64_t n_tokens, int dtype,
                                           const patch_kv8_cache *cache, const int32_t *block_table,
@@ -836,9 +838,11 @@ PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_head
  * p; window > 0 (causal only) also those before p - window + 1.  A query that
  * sees no token gives out = 0 and lse = -inf.  Rows from cu_q[batch] on are
  * left as they were.
- * fp32 scores, softmax statistics and sums; q and the probabilities enter the
- * tensor cores as fp16 (q divided by a power of two of its own row first, so
- * that no finite value overflows).
+ * fp32 scores, softmax statistics and sums.  The probabilities enter the tensor
+ * cores as fp16, and so does q, divided by a power of two of its own row first
+ * so that no finite value overflows; with 64 query rows or more for a sequence
+ * and key/value head on average, q enters as a sum of two (bf16) or three (fp16)
+ * e4m3 numbers instead, exact but for at most 2^-17 of the row's largest element.
  *   q, out     n_tokens rows of heads (q->heads a multiple of kv_heads, at most
  *              16 times), dtype bf16 or fp16; out may be q (same strides)
  *   lse        fp32 [n_tokens][q->heads] or NULL: log sum exp of the scaled scores
@@ -848,9 +852,12 @@ PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_head
  *              sizes on one stream.  Calls that may run at the same time need one each.
  * A page id outside the pool, or kv_lens[b] outside 0 .. max_pages * page, sets
  * PATCH_DEV_BOUNDS (the tokens there read as zeros; the length is clamped).
- * Bounded waits as patch_gemm (wait_limit_us, 0 = 2 s).  dev_status may be NULL.
- * Errors: PATCH_ERR_INVALID_ARG, PATCH_ERR_SHAPE, PATCH_ERR_ALIGN,
- * PATCH_ERR_WORKSPACE, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
+ * Bounded waits as patch_gemm (wait_limit_us, 0 = 2 s); after one that ran out
+ * (PATCH_DEV_TIMEOUT) zero the workspace again.  dev_status may be NULL.
+ * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts, dtype, n_tokens != batch without cu_q, scale not
+ * finite, window < 0 or without causal), PATCH_ERR_SHAPE (page, head_dim, q->heads not a multiple of
+ * kv_heads up to 16 times; n_tokens > 2^26, batch > 2^28, max_pages * page > 2^30, n_pages * kv_heads
+ * >= 2^31), PATCH_ERR_ALIGN, PATCH_ERR_WORKSPACE, PATCH_ERR_DEVICE, PATCH_ERR_CUDA.
  */
 PATCH_API patch_status_t patch_attn_kv8_workspace_size(int64_t n_tokens, int64_t batch, int64_t q_heads,
                                                        const patch_kv8_cache *cache, size_t *bytes);

@@ -52,7 +52,7 @@ def test_rope_refusals(lib):
                dict(q=heads(0), qo=heads(0))):
         assert call(**kw) == 1, kw
     for kw in (dict(D=12), dict(D=132), dict(D=2048), dict(rot=0), dict(rot=24), dict(rot=144), dict(n_pos=0),
-               dict(T=1 << 31)):
+               dict(T=1 << 31), dict(q=heads(65533), qo=heads(65533)), dict(k=heads(1 << 62), ko=heads(1 << 62))):
         assert call(**kw) == 2, kw
     for kw in (dict(q=heads(data=F + 2)), dict(qo=heads(ts=1025)), dict(k=heads(hs=4)), dict(table=F + 8),
                dict(pos=F + 2)):

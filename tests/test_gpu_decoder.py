@@ -371,6 +371,30 @@ def test_attn_prompts(H, Hk, D, page, dtype, kv, q):
     run_attn(len(kv), H, Hk, D, page, kv, q, dtype, causal=False, seed=13, scale=-0.05)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_prompt_scores_of_wide_queries(D, dtype):
+    """One token in view, so lse is its score: with 128-row tiles the queries are sums of e4m3 numbers,
+    off by at most 2^-17 of a row's largest element; D fp32 additions of up to three terms beside."""
+    g, m = gen(31), 300
+    q = torch.randn(m, 1, D, generator=g, device="cuda").double()
+    q *= torch.exp2(-20 * torch.rand(m, 1, D, generator=g, device="cuda").double())
+    q[: m // 2] *= 2.0 ** (100 if dtype == BF16 else 12)
+    q[3], q[4, :, 5], q[5, :, :1] = 0.0, math.inf, math.nan
+    q = q.to(dtype)
+    cache = random_cache(1, 1, 16, D, g)
+    bt, lens, cu = i32([[0]]), i32([1]), i32([0, m])
+    out, lse = tsg.patch_attn_kv8(q, cache, bt, lens, cu, causal=False, want_lse=True)
+    k = cache.k[0, 0, 0].double() * cache.k_scale[0, 0].double()
+    x, f = q[:, 0].double(), 1 / math.sqrt(D)
+    bound = f * (2.0**-17 * x.abs().amax(1) * k.abs().sum() + 3 * (D + 2) * 2.0**-24 * (x.abs() @ k.abs())) + 1e-30
+    want = (x @ k) * f
+    want[4] = math.nan  # an infinite score has no softmax
+    within(lse[:, 0], want, bound, "lse")
+    v = cache.v[0, 0, 0].double() * cache.v_scale[0, 0].double()
+    within(out[:, 0], torch.where(want.isnan()[:, None], math.nan, v.expand(m, D)), 2.0**-8 * v.abs() + 1e-30, "out")
+
+
 def test_attn_bad_lengths_and_pages_read_as_zeros():
     g = gen(8)
     cache = random_cache(4, 2, 16, 64, g)

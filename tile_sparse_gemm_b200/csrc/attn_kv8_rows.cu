@@ -60,6 +60,7 @@ struct RowsCfg {
 };
 
 constexpr float kLeast = 1.0e-37f;  // of a score's factor: not 0, hidden scores are -inf times it
+constexpr float kBig = 16777216.0f;  // of a maximum: from here on its own rounding is one or more
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
 
 // fp32 sums of fp16 (kind::f16) or of e4m3 (kind::f8f6f4): type codes 0 both
@@ -285,6 +286,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
       const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
 
       float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;  // l: of this thread's scores
+      bool big = false;                                           // some row's maximum is
       // elements half * D / 2 on of the row that a NaN value reaches
       uint32_t nan_row[D / 64];
 #pragma unroll
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         if (__any_sync(0xFFFFFFFFu, grow || v_new != v_ref)) {
           const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
           if (grow) m = mx;
+          big = __any_sync(0xFFFFFFFFu, fabsf(m) >= kBig && m != -INFINITY);
           l *= f;
           if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
           const float fo = f * (v_ref * v_inv);
@@ -361,6 +364,14 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         const float base = m == -INFINITY ? 0.0f : m;
         const uint64_t base2 = pack2(-base, -base);
         uint64_t sum[2] = {0, 0};  // of even and odd scores, in turn
+        if (big) {  // round the products as the maximum was rounded: unrounded ones may lie far above it
+#pragma unroll
+          for (int i = 0; i < SL / 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[16 * i + j] = __fmul_rn(s[16 * i + j], kf[i]);
+            kf[i] = 1.0f;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
           const float vr = vs[i] * v_inv;

@@ -81,6 +81,7 @@ patch_status_t patch_rope(const patch_heads* q, const patch_heads* k, const patc
   if (dtype != PATCH_DTYPE_FP32 && !half_type(dtype)) return PATCH_ERR_INVALID_ARG;
   if (layout != PATCH_ROPE_HALF && layout != PATCH_ROPE_INTERLEAVED) return PATCH_ERR_INVALID_ARG;
   if (q->heads != q_out->heads || (k && k->heads != k_out->heads)) return PATCH_ERR_INVALID_ARG;
+  if (q->heads > 65535 || (k && k->heads > 65535 - q->heads)) return PATCH_ERR_SHAPE;  // a launch's grid
   if (n_tokens > kMaxCount || n_pos < 1 || n_pos > kMaxCount || head_dim < 16 || head_dim > 1024 || head_dim % 8 ||
       rot_dim < 16 || rot_dim > head_dim || rot_dim % 16)
     return PATCH_ERR_SHAPE;
