@@ -29,6 +29,11 @@
 // cache row serve directly as its operands, and values are transposed by a
 // byte permute of two tokens' words.  A page's key scale multiplies the scores,
 // its value scale (relative to the largest so far) the probabilities.
+//
+// Measured (32 heads over 8 of 128): 64 sequences of up to 8000 tokens, 502 MB, 95 us
+// (5.3 TB/s; the loop itself runs at 7); one sequence of 131000, 268 MB, 57 us (4.7 TB/s).
+// One of 1500, 32 heads over 32, 12 us: about 5 us until the first bytes are there
+// (launch, lengths, block table, TMA), 2 to work, 3 to join.
 #include <type_traits>
 
 #include "attn_kv8.cuh"

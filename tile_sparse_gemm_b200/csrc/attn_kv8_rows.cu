@@ -2,24 +2,34 @@
 // (chunks of a prompt): tiles of 128 query rows on tcgen05 (include/patch.h:
 // patch_attn_kv8; attn_kv8.cu has the form for few rows and the mathematics).
 //
-// What bounds it: with 128 rows to a tile every cached byte meets 128 rows, so
-// it is bound by computing: two products of 128 x 64 x D a block of 64 tokens,
-// 8192 exponentials, and the conversion of the block to fp16.  Per SM that is
-// about 2 x 256 tensor-core cycles (D = 128), 512 cycles of exponentials and some
-// 700 of other softmax instructions, so the roles run side by side, and two CTAs
-// share an SM:
+// What bounds it: with 128 rows to a tile every cached byte meets 128 rows, so it is
+// bound by computing.  A block of 128 tokens is two products of 128 x 128 x D (2 x 524
+// tensor-core cycles of an SM at D = 128), 16384 exponentials (1024 cycles of the
+// special-function units) and some 700 cycles of other softmax instructions, and
+// the conversion of the values.  The roles run side by side, one CTA per SM (its tensor
+// memory holds two blocks of scores and the sums, its registers 14 warps of 128):
 //   warps 0-7   softmax, two threads per row with half of a block's scores each: scores
 //               from tensor memory, the row's maximum exchanged between the two,
 //               probabilities as fp16 back into the place of the scores, where the second
 //               product takes them.  The sum of the values stays in tensor memory and is
 //               rescaled only when a row's maximum grows by more than 2^8 (probabilities
 //               are at most 2^8 then, well inside fp16; sums are fp32);
-//   warps 8-11  convert the e4m3 block that TMA has brought: keys as they lie, values
-//               transposed (tokens in a row), both in the 128-byte swizzle that the
-//               tensor cores read;
+//   warps 8-11  convert the e4m3 values that TMA has brought to fp16, transposed (tokens
+//               in a row), in the 128-byte swizzle that the tensor cores read;
 //   warp 12     one thread issues the products: S = Q K^T for block g into one of two
 //               places once O += P V of block g - 2, which held that place, is done;
 //   warp 13     fetches: block table, scales, TMA.
+// The keys are multiplied as they lie in the cache, e4m3 by e4m3 (kind::f8f6f4, twice
+// fp16's rate): a query element, scaled so that its row's largest is in [2^7, 2^8), is the
+// sum of two (bf16) or three (fp16) e4m3 numbers, each the rounding of what the ones before
+// leave.  bf16 has 8 bits and fp16 11, an e4m3 number takes off at least 4 of them, so the
+// sum is exact but for what lies below e4m3's smallest step, 2^-10 or 2^-17 of the row's
+// largest.  Two terms take as long as one fp16 product, and the keys need no conversion.
+//
+// Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 334 us,
+// 702 TFLOP/s; 512 queries over 8000: 97 us, 666 TFLOP/s.  A block takes a CTA about 2600
+// cycles: the softmax warps' 1350 for exponentials and probabilities, 220 for the maximum,
+// 210 to exchange it, 390 to read and mask, and their waits; a tile costs 8000 more.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
 // tiles begin and end; a tile cut between CTAs is finished by the last to arrive.
 #include <type_traits>

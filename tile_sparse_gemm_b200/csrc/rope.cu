@@ -53,7 +53,8 @@ cudaError_t launch_rope_table(int64_t n_pos, int half, const RopeTableParams& P,
 // every head.  A unit is one thread's work on one head: V pairs (two 16-byte
 // pieces, V = 8 elements of 16 bits or 4 of 32 each) inside the rotated part, one
 // 16-byte piece behind it.  A thread keeps its unit's V angles in registers and
-// takes kHeads heads with them, their loads under way together.
+// takes kHeads heads with them, their loads under way together.  8192 tokens of
+// 32 + 32 heads of 128 in bf16, 268 MB: 45 us, 5.9 TB/s.
 template <typename T, bool kInterleaved, int kHeads>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams P) {
   constexpr int V = 16 / sizeof(T);
