@@ -26,8 +26,8 @@
 // sum is exact but for what lies below e4m3's smallest step, 2^-10 or 2^-17 of the row's
 // largest.  Two terms take as long as one fp16 product, and the keys need no conversion.
 //
-// Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 334 us,
-// 702 TFLOP/s; 512 queries over 8000: 97 us, 666 TFLOP/s.  A block takes a CTA about 2600
+// Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 329 us,
+// 713 TFLOP/s; 512 queries over 8000: 97 us, 670 TFLOP/s.  A block takes a CTA about 2600
 // cycles: the softmax warps' 1350 for exponentials and probabilities, 220 for the maximum,
 // 210 to exchange it, 390 to read and mask, and their waits; a tile costs 8000 more.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
@@ -70,7 +70,6 @@ struct RowsCfg {
 };
 
 constexpr float kLeast = 1.0e-37f;  // of a score's factor: not 0, hidden scores are -inf times it
-constexpr float kBig = 16777216.0f;  // of a maximum: from here on its own rounding is one or more
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
 
 // fp32 sums of fp16 (kind::f16) or of e4m3 (kind::f8f6f4): type codes 0 both
@@ -296,7 +295,6 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
       const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
 
       float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;  // l: of this thread's scores
-      bool big = false;                                           // some row's maximum is
       // elements half * D / 2 on of the row that a NaN value reaches
       uint32_t nan_row[D / 64];
 #pragma unroll
@@ -321,22 +319,30 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         if (c - 2 >= cur.c) see_nan(c - 2, g - 2);  // these scores have taken the place of its probabilities
         const int t0 = (t.chunk0 + c) * CH + kCols * half;  // of this thread's tokens
         const uint32_t s_at = lanes + (g & 1) * CH + kCols * half;
-        // the slices' key scales (times the row's) and value scales, read before the scores so that their latency is hidden
-        float kf[SL / 2], vs[SL / 2];
+        // the slices' key scales (times the row's), read before the scores so that their latency is hidden
+        const float2* sc = scales + SL * (g & 7) + SL / 2 * half;
+        float kf[SL / 2];
 #pragma unroll
-        for (int i = 0; i < SL / 2; i += 2) {
-          const float4 x = *reinterpret_cast<const float4*>(scales + SL * (g & 7) + SL / 2 * half + i);
-          kf[i] = fmaxf(x.x * row_scale, kLeast), vs[i] = x.y;
-          kf[i + 1] = fmaxf(x.z * row_scale, kLeast), vs[i + 1] = x.w;
-        }
+        for (int i = 0; i < SL / 2; ++i) kf[i] = fmaxf(sc[i].x * row_scale, kLeast);
         const float v_new = fmaxf(v_ref, v_max[g & 7]);
         float s[kCols];  // products; hidden ones -inf
         tmem_ld_64cols(s_at, reinterpret_cast<uint32_t(&)[64]>(s));
-        if (t0 + kCols > all_hi || t0 < all_lo) {
-          const int hi = see_hi - t0, lo = see_lo - t0;
+        // Below, a score is not rounded before the maximum, which is, is taken off; from 2^24 on it could lie far
+        // above it.  Where scores may be that large, round them here.
+        constexpr float kWild = float(16777216.0 / (448.0 * 256.0 * D));
+        float most = kf[0];
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
+        for (int i = 1; i < SL / 2; ++i) most = fmaxf(most, kf[i]);
+        if (t0 + kCols > all_hi || t0 < all_lo || most >= kWild) {
+          const int hi = see_hi - t0, lo = see_lo - t0;
+          const bool wild = most >= kWild;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            if (wild) s[j] = __fmul_rn(s[j], kf[j / 16]);
             if (j >= hi || j < lo) s[j] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < SL / 2; ++i) kf[i] = wild ? 1.0f : kf[i];
         }
         float mx = m;
 #pragma unroll
@@ -352,7 +358,6 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         if (__any_sync(0xFFFFFFFFu, grow || v_new != v_ref)) {
           const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
           if (grow) m = mx;
-          big = __any_sync(0xFFFFFFFFu, fabsf(m) >= kBig && m != -INFINITY);
           l *= f;
           if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
           const float fo = f * (v_ref * v_inv);
@@ -374,17 +379,9 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         const float base = m == -INFINITY ? 0.0f : m;
         const uint64_t base2 = pack2(-base, -base);
         uint64_t sum[2] = {0, 0};  // of even and odd scores, in turn
-        if (big) {  // round the products as the maximum was rounded: unrounded ones may lie far above it
-#pragma unroll
-          for (int i = 0; i < SL / 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s[16 * i + j] = __fmul_rn(s[16 * i + j], kf[i]);
-            kf[i] = 1.0f;
-          }
-        }
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
-          const float vr = vs[i] * v_inv;
+          const float vr = sc[i].y * v_inv;
           const uint64_t k2 = pack2(kf[i], kf[i]), vr2 = pack2(vr, vr);
           uint32_t w[8];
 #pragma unroll
