@@ -9,6 +9,7 @@ extension of the decode step's calls beside it.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -47,12 +48,11 @@ def build_binding(force: bool = False) -> Path:
     """_decoder_binding.so: against this interpreter's and this torch's headers."""
     import torch
 
-    src = CSRC / "decoder_binding.cpp"
+    src, home = CSRC / "decoder_binding.cpp", Path(torch.__file__).resolve().parent
     if not force and BINDING.exists() and all(d.stat().st_mtime <= BINDING.stat().st_mtime
-                                              for d in (src, INCLUDE / "patch.h")):
+                                              for d in (src, INCLUDE / "patch.h", home / "version.py")):
         return BINDING
-    home = Path(torch.__file__).resolve().parent
-    cuda = Path(_nvcc()).parent.parent
+    cuda = Path(shutil.which(_nvcc()) or _nvcc()).parent.parent
     includes = [INCLUDE, home / "include", home / "include/torch/csrc/api/include", sysconfig.get_paths()["include"],
                 cuda / "include"]
     tmp = BINDING.with_suffix(f".so.{os.getpid()}.tmp")

@@ -81,9 +81,14 @@ def _fast():
     """The compiled extension, bound to the library's entry points."""
     global _binding
     if _binding is None:
-        from . import _decoder_binding
+        library = lib()
+        try:
+            from . import _decoder_binding
+        except ImportError as e:
+            raise ImportError("the compiled binding is missing or was built for another torch: build it with "
+                              "`python -m tile_sparse_gemm_b200.build`") from e
 
-        _decoder_binding.bind(*(ctypes.cast(getattr(lib(), "patch_" + f), ctypes.c_void_p).value
+        _decoder_binding.bind(*(ctypes.cast(getattr(library, "patch_" + f), ctypes.c_void_p).value
                                 for f in ("rope", "kv8_append", "attn_kv8", "gemm4")))
         _binding = _decoder_binding
     return _binding
