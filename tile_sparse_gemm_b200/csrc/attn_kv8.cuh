@@ -59,11 +59,17 @@ __device__ __forceinline__ void sequence(const AttnParams& a, int b, int& len, i
   len = int(min(int64_t(max(a.kv_lens[b], 0)), a.max_pages * a.page));
 }
 
+// x / G, the rows of a token: a shift for powers of two (a division's latency is most of what a tile costs
+// in the sums below)
+__device__ __forceinline__ int by_group(int x, int G) {
+  return (G & (G - 1)) == 0 ? x >> (31 - __clz(G)) : x / G;
+}
+
 template <int CH, int R>
 __device__ __forceinline__ void set_rows(const AttnParams& a, int G, Tile& t) {
   int hi = t.len, lo = 0;
-  if (a.causal) hi = max(0, min(t.len, t.len - t.m + min(t.m - 1, (t.rt * R + R - 1) / G) + 1));
-  if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + t.rt * R / G - a.window + 1));
+  if (a.causal) hi = max(0, min(t.len, t.len - t.m + min(t.m - 1, by_group(t.rt * R + R - 1, G)) + 1));
+  if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + by_group(t.rt * R, G) - a.window + 1));
   t.hi = hi;
   t.chunk0 = lo / CH;
   t.chunks = max(1, (hi + CH - 1) / CH - t.chunk0);
@@ -93,6 +99,7 @@ __device__ __forceinline__ int64_t units_per_head(const AttnParams& a, int G, Ti
     return int64_t(n) * (t.chunks + tile_units<R>());
   }
   int64_t s = 0;
+#pragma unroll 4
   for (t.rt = 0; t.rt < n; ++t.rt) {
     set_rows<CH, R>(a, G, t);
     s += t.chunks + tile_units<R>();
