@@ -460,6 +460,17 @@ def test_gemm4(N, K, group, sdtype, dtype):
     assert tsg.patch_gemm4(x[:0], w).shape == (0, N)
 
 
+@pytest.mark.parametrize("M", [1, 11])
+@pytest.mark.parametrize("N,K,group", [(40000, 128, 32), (30011, 320, 64), (30000, 1824, 32)])
+def test_gemm4_many_rows_of_few_blocks(N, K, group, M):
+    """Fewer blocks of 256 k than warps that share them, and several row groups a CTA."""
+    g = gen(N + K)
+    w = tsg.Weight4(torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                    (0.5 + torch.rand(N, K // group, generator=g, device="cuda")).to(BF16), group)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    within(tsg.patch_gemm4(x, w), *ref.gemm4(x, w.codes, w.scales, group))
+
+
 def test_gemm4_rows_with_infinities_and_nan():
     g = gen(2)
     w = tsg.patch_quantize4(torch.randn(40, 256, generator=g, device="cuda"), 64)

@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
     for (;; next = true) {
       if (next) {
         fet.blk = kw;
-        if (!slices && fet.chunk0 + fet.i + 2 < groups) {  // the common case: the next group, of two whole tiles
+        // the common case: the next group, of two whole tiles (and a warp that has blocks: else no place is set)
+        if (kw < fet.nb && !slices && fet.chunk0 + fet.i + 2 < groups) {
           ++fet.i;
           fet.tile += 2;
           fet.src += int64_t(2 * 16) * row_groups;
