@@ -460,6 +460,20 @@ def test_gemm4(N, K, group, sdtype, dtype):
     assert tsg.patch_gemm4(x[:0], w).shape == (0, N)
 
 
+@pytest.mark.parametrize("M,N,K,group", [(14, 577, 11072, 64), (9, 2366, 4192, 32), (8, 4096, 14336, 128), (16, 1000, 14336, 64),
+                                         (1, 256, 14336, 128), (4, 2000, 12320, 32), (16, 3000, 8192, 128), (1, 33, 2048, 64)])
+def test_gemm4_parts_of_k(M, N, K, group):
+    """Few rows or many tokens: clusters of CTAs with a part of K each."""
+    g = gen(N + K)
+    w = tsg.Weight4(torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                    (0.5 + torch.rand(N, K // group, generator=g, device="cuda")).to(FP16), group)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    y = tsg.patch_gemm4(x, w)
+    within(y, *ref.gemm4(x, w.codes, w.scales, group))
+    for _ in range(20):
+        assert torch.equal(tsg.patch_gemm4(x, w), y)
+
+
 @pytest.mark.parametrize("M", [1, 11])
 @pytest.mark.parametrize("N,K,group", [(40000, 128, 32), (30011, 320, 64), (30000, 1824, 32)])
 def test_gemm4_many_rows_of_few_blocks(N, K, group, M):

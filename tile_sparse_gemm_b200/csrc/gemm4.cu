@@ -100,6 +100,11 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // warps for either tile, one CTA per SM.  K beyond what X's place holds is taken
 // in slices, the sums of four row groups kept meanwhile by the threads that add them.
 //
+// Every CTA prepares all of X that it needs, which for few rows or many tokens takes
+// longer than the products.  So up to 8 CTAs may form a cluster: they share row groups,
+// each has its part of K (and of X), and their sums are added through distributed shared
+// memory, in the order of the parts.
+//
 // Measured: 128000 x 4096, 1 token, group 32: 69 us (codes and scales, 295 MB, at 4.3
 // TB/s; fetching alone takes 46 us, the rest is what the integer and tensor instructions
 // of a block take beyond that); 14336 x 4096, 16 tokens: 23.5 us, of which 5 prepare X in
@@ -115,10 +120,12 @@ struct Params {
   int32_t* status;
   int N, K, M, dtype;
   int blocks, slice_blocks, tiles, chunk;  // 256-k blocks of K and of a slice; row tiles; row groups of a CTA at a time
+  int parts;                               // of K: CTAs of a cluster
 };
 
 constexpr int kKWarps = 8;  // warps that share a row tile's blocks of k
 constexpr int kGroupRows = 32;
+constexpr int kMaxParts = 8;  // the portable size of a cluster
 constexpr int kKept = 4;  // row groups whose sums are kept over slices, in registers
 
 template <int NT>
@@ -166,6 +173,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float load_of_cta(uint32_t addr, int rank) {  // the word at this shared address of a cluster's CTA
+  uint32_t there;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+  return v;
+}
 // S: type of the scales; NT: 8-token tiles; GS: log2 of the group.
 template <typename S, int NT, int GS>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
@@ -176,7 +192,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q = lane & 3;
   const int kw = warp % kKWarps, rw = warp / kKWarps;
-  const bool slices = P.slice_blocks < P.blocks;
+  const int parts = P.parts, part = parts > 1 ? int(blockIdx.x) % parts : 0;  // clusters are CTAs in a row
+  const int kb0 = int(int64_t(P.blocks) * part / parts);                     // this CTA's blocks of K: kb0 on
+  const int blocks = int(int64_t(P.blocks) * (part + 1) / parts) - kb0;
+  const bool slices = P.slice_blocks < blocks;
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   uint4* xs = reinterpret_cast<uint4*>(smem + L.x);
   float* neg_sum = reinterpret_cast<float*>(smem + L.neg_sum);
@@ -199,10 +218,11 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   // This CTA's row tiles are tile0 .. tile1 - 1, two of them a row group, `chunk` groups at a
   // time; for these, slice after slice, the warp's blocks are kw, kw + kKWarps, ... of the
   // slice.  The cursor of what is fetched next runs ahead through the same order.
-  const int tile0 = int(int64_t(P.tiles) * blockIdx.x / gridDim.x);
-  const int tile1 = int(int64_t(P.tiles) * (blockIdx.x + 1) / gridDim.x);
+  const int n_shares = int(gridDim.x) / parts, share = int(blockIdx.x) / parts;
+  const int tile0 = int(int64_t(P.tiles) * share / n_shares);
+  const int tile1 = int(int64_t(P.tiles) * (share + 1) / n_shares);
   const int groups = (tile1 - tile0 + 1) / 2;
-  auto nb_of = [&](int b0) { return min(P.slice_blocks, P.blocks - b0); };
+  auto nb_of = [&](int b0) { return min(P.slice_blocks, blocks - b0); };
   const int row_groups = P.K >> GS;
   const bool vec = P.K % kBlockK == 0;  // then a block's scales of a row are one aligned piece
   struct {
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
         if (++fet.i >= P.chunk || fet.chunk0 + fet.i >= groups) {
           fet.i = 0;
           fet.b0 += P.slice_blocks;
-          if (fet.b0 >= P.blocks) {
+          if (fet.b0 >= blocks) {
             fet.b0 = 0;
             fet.chunk0 += P.chunk;
           }
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
     }
     fet.tile = tile0 + (fet.chunk0 + fet.i) * 2 + rw;
     fet.boxes = max(min(MT, tile1 - fet.tile), 0);  // a last group may have one tile only: the other's sums are not stored
-    fet.src = static_cast<const S*>(P.scales) + int64_t(min(16 * fet.tile + lane, P.N - 1)) * row_groups + fet.b0 * kGroups;
+    fet.src = static_cast<const S*>(P.scales) + int64_t(min(16 * fet.tile + lane, P.N - 1)) * row_groups + (kb0 + fet.b0) * kGroups;
   };
   settle(false);
   int issued = 0, done = 0;
@@ -249,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
         else
           tc::mbar_arrive(bars + st);
         uint8_t* dst = smem + (warp * kStages + st) * C::kStageBytes;
-        const int x = (fet.b0 + fet.blk) * 128;
+        const int x = (kb0 + fet.b0 + fet.blk) * 128;
         if (fet.boxes > 0) tc::tma_load_2d(dst, &P.codes, bars + st, x, fet.tile * 16);
         if (fet.boxes > 1) tc::tma_load_2d(dst + kBoxBytes, &P.codes, bars + st, x, fet.tile * 16 + 16);
       }
@@ -260,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(kScaleRow)
                        : "memory");
         } else {
-          const int left = row_groups - (fet.b0 + fet.blk) * kGroups;
+          const int left = row_groups - (kb0 + fet.b0 + fet.blk) * kGroups;
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) dst[g] = g < left ? src[g] : from_f32<S>(0.0f);
         }
@@ -285,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
 
   float kept[kKept] = {};
   for (int chunk0 = 0; chunk0 < groups; chunk0 += P.chunk) {
-    for (int b0 = 0; b0 < P.blocks; b0 += P.slice_blocks) {
+    for (int b0 = 0; b0 < blocks; b0 += P.slice_blocks) {
       const int nb = nb_of(b0);
       // ---- X of the slice: 16 threads per token and 128 k
       if (slices || chunk0 == 0) {
@@ -301,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
           for (int j = 0; j < kAhead; ++j) {
             ms[j] = m;
             us[j] = at;
-            const int k = b0 * kBlockK + at * 8;
+            const int k = (kb0 + b0) * kBlockK + at * 8;
             raw[j] = make_uint4(0, 0, 0, 0);
             if (m < P.M && k < P.K)
               raw[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.X) + int64_t(m) * P.K + k);
@@ -434,7 +454,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
         }
         // ---- add the warps' sums: [kw][token][row of the group]
         const int outs = P.M * kGroupRows;
-        __syncthreads();  // the last ones are read
+        if (parts == 1)
+          __syncthreads();  // the last ones are read
+        else if (chunk0 + i > 0)
+          cluster_wait();  // by the cluster's other CTAs too
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -456,8 +479,25 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
           for (int j = 0; j + 1 < kKept; ++j) kept[j] = kept[j + 1];  // with slices, a chunk is kKept groups at most:
           kept[kKept - 1] = v;                                       // the next slice finds this one's sum first
           const int row = row0 + o % kGroupRows;
-          if (b0 + nb == P.blocks && row < P.N && row < 16 * tile1)
+          if (parts > 1)
+            reduce[o] = v;  // this thread alone has read the word
+          else if (b0 + nb == blocks && row < P.N && row < 16 * tile1)
             store_y(static_cast<uint16_t*>(P.Y) + int64_t(o / kGroupRows) * P.N + row, v * 4096.0f, P.dtype);
+        }
+        if (parts > 1) {  // no slices then: each CTA adds and stores its share of the group's outputs
+          __syncwarp();
+          cluster_arrive();
+          cluster_wait();
+          const int o1 = outs * (part + 1) / parts, ox = outs * part / parts + int(threadIdx.x);
+          if (ox < o1) {
+            float v = 0.0f;
+            for (int r = 0; r < parts; ++r) v += load_of_cta(tc::smem_u32(reduce + ox), r);
+            const int row = row0 + ox % kGroupRows;
+            if (row < P.N && row < 16 * tile1)
+              store_y(static_cast<uint16_t*>(P.Y) + int64_t(ox / kGroupRows) * P.N + row, v * 4096.0f, P.dtype);
+          }
+          __syncwarp();
+          cluster_arrive();
         }
       }
       for (int i = n_here; i < kKept; ++i) {  // turn a shorter chunk's sums round as well
@@ -471,6 +511,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   // after a timeout: let the copies in flight land before the shared memory goes
   for (; done < issued; ++done)
     tc::wait_bounded(bars + done % kStages, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, true);
+  __syncwarp();
+  if (parts > 1) cluster_wait();  // the others have read this CTA's sums
 }
 
 template <typename S, int NT, int GS>
@@ -478,18 +520,41 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   using C = Cfg<NT>;
   P.tiles = (P.N + 15) / 16;
   P.blocks = (P.K + kBlockK - 1) / kBlockK;
-  const int grid = P.tiles < C::kCtas * num_sms ? P.tiles : C::kCtas * num_sms;
-  const int per_cta = ((P.tiles + grid - 1) / grid + 1) / 2;
   // a slice: whole rounds of the warps, as many as fit
   const int fit = C::kXBytes / P.M / (kBlockK * 2) / kKWarps * kKWarps;
-  const bool slices = P.blocks > fit;
-  P.slice_blocks = slices ? fit : P.blocks;
-  P.chunk = slices && per_cta > kKept ? kKept : per_cta;
+  // Parts of K, by an estimate of a CTA's time in ns: X of a block and token 20 (again for every chunk of row groups
+  // where K is taken in slices), a row group's products of a block 165 (both tiles' warps) or 300 (two CTAs an SM),
+  // its sums 300, 1500 with each slice, or 2200 through the cluster.  Measured with one part and with the chosen:
+  // 577 x 11072, 14 tokens 31 us, 12 (4 parts); 4096 x 14336, 8 tokens 39, 20 (8), 16 tokens 37, 25 (4); 256 x
+  // 14336, 1 token 12.3, 6.4 (8); 4096 x 4096, 1 token 7.1, 6.4 (2).  One part stays where the others lose: 4096 x
+  // 4096, 16 tokens 11.9, 12.3 with two; 14336 x 4096, 16 tokens 23, 28; 128000 x 4096, 1 token 66, 107.
+  float best = 0.0f;
+  int grid = 0;
+  for (int parts = 1; parts <= kMaxParts && parts <= P.blocks; parts *= 2) {
+    const int local = (P.blocks + parts - 1) / parts;
+    // clusters that run at once: they lie in one of the GPU's parts of 16 to 20 SMs each (33 of 4, 15 of 8 on 148 SMs)
+    const int most = C::kCtas * num_sms * (parts <= 2 ? 16 : parts == 4 ? 14 : 13) / 16 / parts;
+    const bool slices = local > fit;
+    if (parts > 1 && (slices || most < 1)) continue;
+    const int shares = P.tiles < most ? P.tiles : most, groups = ((P.tiles + shares - 1) / shares + 1) / 2;
+    const float times = slices ? float((groups + kKept - 1) / kKept) : 1.0f;
+    const float sums = parts > 1 ? 2200.0f : slices ? 300.0f + 1500.0f * float((local + fit - 1) / fit) : 300.0f;
+    const float ns = 20.0f * float(P.M) * float(local) * times +
+                     float(groups) * ((NT == 1 ? 300.0f : 165.0f) * float(local) + sums);
+    if (parts > 1 && ns >= best) continue;
+    best = ns;
+    grid = shares * parts;
+    P.parts = parts;
+    P.slice_blocks = slices ? fit : local;
+    P.chunk = slices && groups > kKept ? kKept : groups;
+  }
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   auto kernel = gemm4_kernel<S, NT, GS>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(unsigned(grid)), dim3(C::kThreads), size_t(L.bytes), stream, P);
+  const dim3 grid_dim{unsigned(grid)}, block_dim{C::kThreads};
+  return P.parts == 1 ? launch_pdl(kernel, grid_dim, block_dim, size_t(L.bytes), stream, P)
+                      : launch_pdl_cluster(kernel, grid_dim, block_dim, size_t(L.bytes), stream, unsigned(P.parts), P);
 }
 
 template <typename S, int NT>
