@@ -371,6 +371,19 @@ def test_attn_prompts(H, Hk, D, page, dtype, kv, q):
     run_attn(len(kv), H, Hk, D, page, kv, q, dtype, causal=False, seed=13, scale=-0.05)
 
 
+@pytest.mark.parametrize("B", [257, 449, 1000])
+@pytest.mark.parametrize("many", [False, True])
+def test_attn_more_sequences_than_threads(B, many):
+    """Shares of the work are found by a CTA of 256 or 448 threads, a sequence each at a time."""
+    q_lens = [(7 * i) % 23 + 10 * many for i in range(B)] if many else [i % 3 for i in range(B)]
+    run_attn(B, 8, 1, 64, 16, [n + (5 * i) % 40 for i, n in enumerate(q_lens)], q_lens, FP16)
+
+
+def test_append_more_sequences_than_threads():
+    past, new = [(11 * i) % 37 for i in range(700)], [(5 * i) % 4 for i in range(700)]
+    test_append(16, 64, 2, BF16, "half", 64, past, new)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("D", [64, 128])
 def test_attn_prompt_scores_of_wide_queries(D, dtype):
