@@ -105,10 +105,10 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // each has its part of K (and of X), and their sums are added through distributed shared
 // memory, in the order of the parts.
 //
-// Measured: 128000 x 4096, 1 token, group 32: 69 us (codes and scales, 295 MB, at 4.3
+// Measured: 128000 x 4096, 1 token, group 32: 67 us (codes and scales, 295 MB, at 4.4
 // TB/s; fetching alone takes 46 us, the rest is what the integer and tensor instructions
 // of a block take beyond that); 14336 x 4096, 16 tokens: 23.5 us, of which 5 prepare X in
-// every CTA and 11 are the products; 4096 x 4096, 1 token: 6.5 us, mostly latency.
+// every CTA and 11 are the products; 4096 x 4096, 1 token: 6.2 us, mostly latency.
 namespace g4 {
 
 constexpr int kBlockK = 256, kBoxBytes = 16 * 128;
@@ -182,8 +182,9 @@ __device__ __forceinline__ float load_of_cta(uint32_t addr, int rank) {  // the 
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
   return v;
 }
-// S: type of the scales; NT: 8-token tiles; GS: log2 of the group.
-template <typename S, int NT, int GS>
+// S: type of the scales; NT: 8-token tiles; GS: log2 of the group; kParts: K is split over a cluster (its own kernel:
+// the checks in one for both take 128000 x 4096 from 67 to 71 us).
+template <typename S, int NT, int GS, bool kParts>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
   using C = Cfg<NT>;
   constexpr int kWarps = C::kWarps, kStages = C::kStages, MT = C::MT;
@@ -192,10 +193,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q = lane & 3;
   const int kw = warp % kKWarps, rw = warp / kKWarps;
-  const int parts = P.parts, part = parts > 1 ? int(blockIdx.x) % parts : 0;  // clusters are CTAs in a row
+  const int parts = kParts ? P.parts : 1, part = kParts ? int(blockIdx.x) % parts : 0;  // clusters are CTAs in a row
   const int kb0 = int(int64_t(P.blocks) * part / parts);                     // this CTA's blocks of K: kb0 on
   const int blocks = int(int64_t(P.blocks) * (part + 1) / parts) - kb0;
-  const bool slices = P.slice_blocks < blocks;
+  const bool slices = !kParts && P.slice_blocks < blocks;
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   uint4* xs = reinterpret_cast<uint4*>(smem + L.x);
   float* neg_sum = reinterpret_cast<float*>(smem + L.neg_sum);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
         }
         // ---- add the warps' sums: [kw][token][row of the group]
         const int outs = P.M * kGroupRows;
-        if (parts == 1)
+        if (!kParts)
           __syncthreads();  // the last ones are read
         else if (chunk0 + i > 0)
           cluster_wait();  // by the cluster's other CTAs too
@@ -479,12 +480,12 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
           for (int j = 0; j + 1 < kKept; ++j) kept[j] = kept[j + 1];  // with slices, a chunk is kKept groups at most:
           kept[kKept - 1] = v;                                       // the next slice finds this one's sum first
           const int row = row0 + o % kGroupRows;
-          if (parts > 1)
+          if (kParts)
             reduce[o] = v;  // this thread alone has read the word
           else if (b0 + nb == blocks && row < P.N && row < 16 * tile1)
             store_y(static_cast<uint16_t*>(P.Y) + int64_t(o / kGroupRows) * P.N + row, v * 4096.0f, P.dtype);
         }
-        if (parts > 1) {  // no slices then: each CTA adds and stores its share of the group's outputs
+        if (kParts) {  // no slices then: each CTA adds and stores its share of the group's outputs
           __syncwarp();
           cluster_arrive();
           cluster_wait();
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   for (; done < issued; ++done)
     tc::wait_bounded(bars + done % kStages, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, true);
   __syncwarp();
-  if (parts > 1) cluster_wait();  // the others have read this CTA's sums
+  if (kParts) cluster_wait();  // the others have read this CTA's sums
 }
 
 template <typename S, int NT, int GS>
@@ -549,7 +550,7 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
     P.chunk = slices && groups > kKept ? kKept : groups;
   }
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
-  auto kernel = gemm4_kernel<S, NT, GS>;
+  auto kernel = P.parts > 1 ? gemm4_kernel<S, NT, GS, true> : gemm4_kernel<S, NT, GS, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid_dim{unsigned(grid)}, block_dim{C::kThreads};
