@@ -105,7 +105,7 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // each has its part of K (and of X), and their sums are added through distributed shared
 // memory, in the order of the parts.
 //
-// Measured: 128000 x 4096, 1 token, group 32: 67 us (codes and scales, 295 MB, at 4.4
+// Measured: 128000 x 4096, 1 token, group 32: 69 us (codes and scales, 295 MB, at 4.3
 // TB/s; fetching alone takes 46 us, the rest is what the integer and tensor instructions
 // of a block take beyond that); 14336 x 4096, 16 tokens: 23.5 us, of which 5 prepare X in
 // every CTA and 11 are the products; 4096 x 4096, 1 token: 6.2 us, mostly latency.
@@ -182,9 +182,10 @@ __device__ __forceinline__ float load_of_cta(uint32_t addr, int rank) {  // the 
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
   return v;
 }
-// S: type of the scales; NT: 8-token tiles; GS: log2 of the group; kParts: K is split over a cluster (its own kernel:
-// the checks in one for both take 128000 x 4096 from 67 to 71 us).
-template <typename S, int NT, int GS, bool kParts>
+// S: type of the scales; NT: 8-token tiles; GS: log2 of the group; kParts: K is split over a cluster; kVec: K is a
+// multiple of kBlockK, so that a block's scales of a row are one aligned piece.  The last two are kernels of their own:
+// in a row of launches 128000 x 4096 takes 62 us, with kVec's checks in one kernel for both 64, with kParts' 66.
+template <typename S, int NT, int GS, bool kParts, bool kVec>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
   using C = Cfg<NT>;
   constexpr int kWarps = C::kWarps, kStages = C::kStages, MT = C::MT;
@@ -225,7 +226,6 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   const int groups = (tile1 - tile0 + 1) / 2;
   auto nb_of = [&](int b0) { return min(P.slice_blocks, blocks - b0); };
   const int row_groups = P.K >> GS;
-  const bool vec = P.K % kBlockK == 0;  // then a block's scales of a row are one aligned piece
   struct {
     int chunk0, b0, i, blk;  // first group of the chunk, first block of the slice, group of the chunk, block of the slice
     int nb, tile, boxes;     // blocks of the slice, the warp's first tile and how many it has
@@ -277,13 +277,21 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
       if (lane < 16 * MT) {  // a row's scales each
         const S* src = fet.src + fet.blk * kGroups;
         S* dst = reinterpret_cast<S*>(scales + (st * MT * 16 + lane) * kScaleRow);
-        if (vec) {
+        if constexpr (kVec) {
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(kScaleRow)
                        : "memory");
         } else {
           const int left = row_groups - (kb0 + fet.b0 + fet.blk) * kGroups;
+          if (row_groups % 2 == 0) {  // rows of whole words: asynchronous as well, zeros behind K (29573 x 9600: 112 -> 93 us)
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) dst[g] = g < left ? src[g] : from_f32<S>(0.0f);
+            for (int g = 0; g < kGroups; g += 2)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst + g)),
+                           "l"(g < left ? src + g : fet.src), "r"(g < left ? 4 : 0)
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) dst[g] = g < left ? src[g] : from_f32<S>(0.0f);
+          }
         }
       }
       ++issued;
@@ -550,7 +558,10 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
     P.chunk = slices && groups > kKept ? kKept : groups;
   }
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
-  auto kernel = P.parts > 1 ? gemm4_kernel<S, NT, GS, true> : gemm4_kernel<S, NT, GS, false>;
+  const bool vec = P.K % kBlockK == 0;
+  auto kernel = P.parts > 1 ? vec ? gemm4_kernel<S, NT, GS, true, true> : gemm4_kernel<S, NT, GS, true, false>
+                : vec       ? gemm4_kernel<S, NT, GS, false, true>
+                            : gemm4_kernel<S, NT, GS, false, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid_dim{unsigned(grid)}, block_dim{C::kThreads};
