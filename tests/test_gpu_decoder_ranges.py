@@ -1,0 +1,132 @@
+"""The decoder-layer operators at the ends of their ranges: page scales far apart, values near a type's limits."""
+import math
+
+import pytest
+import torch
+
+import _decoder_ref as ref
+import tile_sparse_gemm_b200 as tsg
+from test_gpu_decoder import F8, copy_of, gen, i32, pages_of, random_cache, within
+
+pytestmark = pytest.mark.gpu
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+# (queries per sequence, query heads, key/value heads): tiles of 8, 16 and 128 rows
+TILES = [(1, 4, 2), (3, 8, 2), (90, 2, 1)]
+
+
+def attention_of_own(q, c, bt, kv, m, scale, causal, window):
+    """(out, lse, bound) in 64 bits; m queries a sequence.  A token's part p |v| is off by what its own
+    probability is: fp16 rounds it by 2^-11 or, small beside the sequence's largest, by 2^-25 of that, never by
+    more than itself; fp32 scores and sums add 2^-11 at most.  Another page's values have no part in it."""
+    T, H, D = q.shape
+    hk, page = c.k.shape[1:3]
+    g = H // hk
+    out, bound = torch.zeros(T, H, D, dtype=torch.float64, device="cuda"), torch.zeros(T, H, D, dtype=torch.float64, device="cuda")
+    lse = torch.full((T, H), -math.inf, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(kv):
+        at, pos = torch.arange(n, device="cuda"), torch.arange(n - m, n, device="cuda")[:, None]
+        hidden = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+        hidden |= (at > pos) if causal else False
+        hidden |= (at <= pos - window) if window else False
+        lo = 0 if not window else max(0, n - m - window + 1)  # pages before it may be anywhere
+        ids = bt[b, : -(-n // page)].long()
+        ids[: lo // page] = 0
+        k, v = ((x.view(torch.uint8)[ids].view(F8).double() * s[ids].double()[..., None, None]).transpose(0, 1).reshape(hk, -1, D)[:, :n]
+                for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+        rows = slice(b * m, (b + 1) * m)
+        s = torch.einsum("mhgd,hnd->mhgn", q[rows].double().view(m, hk, g, D), k) * scale
+        s = s.masked_fill(hidden[:, None, None, :].expand_as(s), -math.inf)
+        ls = torch.logsumexp(s, -1)
+        p = torch.exp(s - ls[..., None].nan_to_num(neginf=0.0))
+        off = 2.0**-10 * p + torch.minimum(p, 2.0**-25 * p.amax(-1, keepdim=True))
+        out[rows] = torch.einsum("mhgn,hnd->mhgd", p, v).reshape(m, H, D)
+        bound[rows] = torch.einsum("mhgn,hnd->mhgd", off, v.abs()).reshape(m, H, D)
+        lse[rows] = ls.reshape(m, H)
+    return out, lse, bound + ref.HALF[q.dtype] * out.abs() + ref.TINY[q.dtype]
+
+
+def attend(tile, D, dtype, edit, page=16, kv=(700, 333), causal=True, window=0, scale=None, seed=0):
+    m, H, hk = tile
+    g = gen(seed)
+    bt, n_pages = pages_of(list(kv), page, g)
+    c = random_cache(n_pages, hk, page, D, g)
+    q = torch.randn(m * len(kv), H, D, generator=g, device="cuda").to(dtype)
+    q = edit(q, c, bt)
+    st = tsg.new_status()
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    cu = i32([m * i for i in range(len(kv) + 1)])
+    out, lse = tsg.patch_attn_kv8(q, c, bt, i32(list(kv)), cu, scale, causal, window, want_lse=True, status=st)
+    assert tsg.patch_read_status(st) == (0, 0)
+    want, wl, bound = attention_of_own(q, c, bt, kv, m, scale, causal, window)
+    within(out, want, bound, "out")
+    near = (lse.double() - wl).abs() <= 2.0**-12 * (1 + wl.abs())
+    assert bool((near | (lse.double() == wl)).all())
+    return out, c, bt
+
+
+@pytest.mark.parametrize("far", [12, 20, 24, 40, 90, 119])
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, FP16)])
+@pytest.mark.parametrize("tile", TILES)
+def test_attn_values_under_a_large_scale_without_weight(tile, D, dtype, far):
+    """A page whose values have a scale up to 2^119 and no weight to speak of: the others keep their bits."""
+    def edit(q, c, bt):
+        q[..., 0] = 8.0
+        for b, j in ((0, 3), (0, 30), (1, 0)):
+            ids = int(bt[b, j])
+            c.k[ids] = torch.zeros_like(c.k[ids].float()).to(F8)
+            c.k[ids, :, :, 0] = torch.full_like(c.k[ids, :, :, 0].float(), -256.0).to(F8)
+            c.k_scale[ids] = 16.0  # scores of -2896 and less: probabilities of 0 in any format
+            c.v_scale[ids] = 2.0**far
+        return q
+    attend(tile, D, dtype, edit)
+
+
+@pytest.mark.parametrize("spread", [6, 15, 30, 60])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("D,dtype", [(128, FP16), (64, BF16)])
+@pytest.mark.parametrize("tile", TILES)
+def test_attn_values_under_scales_far_apart(tile, D, dtype, page, spread):
+    """Value scales over 2^-spread .. 2^spread, page by page, each page's scores falling with its scale so that small
+    ones count; elements of the large pages are zero in half of the columns, where nothing hides the small ones."""
+    def edit(q, c, bt):
+        g = gen(spread)
+        e = torch.randint(-spread, spread + 1, c.v_scale.shape, generator=g, device="cuda").float()
+        e -= max(0, spread - 6) if dtype is FP16 else 0  # results within the type
+        c.v_scale.copy_(2.0**e)
+        v = c.v.float()
+        v[..., ::2] *= (e <= 0)[..., None, None]
+        c.v.copy_(v.to(F8))
+        return q
+    attend(tile, D, dtype, edit, page=page, seed=1)
+    attend(tile, D, dtype, edit, page=page, causal=False, seed=2)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_attn_values_under_the_least_and_largest_scales(tile):
+    def edit(low, high):
+        def f(q, c, bt):
+            c.v_scale.fill_(2.0**-5)
+            c.v_scale[bt[0, ::3].long()] = low
+            c.v_scale[bt[1, 1::2].long()] = high
+            return q
+        return f
+    attend(tile, 128, BF16, edit(2.0**-100, 2.0**100), seed=3)  # pages of zeros have the least scale
+    attend(tile, 64, BF16, edit(2.0**100, 2.0**-100), seed=4)
+
+    def first(value):
+        def f(q, c, bt):
+            c.v_scale.fill_(2.0**-5)
+            c.v_scale[bt[:, 0].long()] = value
+            return q
+        return f
+    for value in (0.0, 2.0**-100, 2.0**-30, 2.0**30, 2.0**110):
+        attend(tile, 128, BF16, first(value), seed=5)
+
+    def alone(value):
+        def f(q, c, bt):
+            c.v_scale.fill_(value)
+            return q
+        return f
+    for value in (2.0**-100, 2.0**-60, 2.0**40, 2.0**100):
+        attend(tile, 64, BF16, alone(value), seed=6)

@@ -28,7 +28,8 @@
 // index of a product may run in any order: each lane's 16-byte pieces of a
 // cache row serve directly as its operands, and values are transposed by a
 // byte permute of two tokens' words.  A page's key scale multiplies the scores,
-// its value scale (relative to the largest so far) the probabilities.
+// its value scale (in units of a power of two near the tile's first) the probabilities;
+// what fp16 cannot hold with all its bits there is weighed in fp32 (`apart` below).
 //
 // Measured (32 heads over 8 of 128): 64 sequences of up to 8000 tokens, 502 MB, 95 us
 // (5.3 TB/s; the loop itself runs at 7); one sequence of 131000, 268 MB, 57 us (4.7 TB/s).
@@ -44,6 +45,7 @@ namespace attn {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunkBytes = 4096;  // of keys, and of values
+constexpr float kUnits = 32768.0f;  // of value scales: 2^15, times a probability within fp16
 
 struct Params {
   CUtensorMap k_map, v_map;
@@ -273,15 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
       }
       // ---- softmax
       const bool some_hidden = t0 + CH > all_hi || t0 < all_lo;
-      float mx[NT][2], v_new = v_ref, vs[SL];
+      float mx[NT][2], vs[SL], v_hi = 0.0f, v_lo = INFINITY;  // value scales; the largest, and the smallest but 0
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mx[nt][0] = m[nt][0], mx[nt][1] = m[nt][1];
 #pragma unroll
       for (int sl = 0; sl < SL; ++sl) {
         const float2 sc = *reinterpret_cast<const float2*>(scales + st * 8 + 2 * ((16 * sl) >> P.box_shift));
         vs[sl] = sc.y;
-        if (some_hidden && t0 + 16 * sl >= t.hi) vs[sl] = 0.0f;  // seen by no row and perhaps not fetched
-        v_new = fmaxf(v_new, vs[sl]);
+        // seen by no row, perhaps not fetched
+        if (some_hidden && (t0 + 16 * sl >= t.hi || t0 + 16 * sl + 16 <= t.lo)) vs[sl] = 0.0f;
+        v_hi = fmaxf(v_hi, vs[sl]);
+        if (vs[sl] > 0.0f) v_lo = fminf(v_lo, vs[sl]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -304,6 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx[nt][i & 1] = fmaxf(mx[nt][i & 1], s[sl][nt][i]);
+      // O is in units of v_ref, 2^8 below the first scale.  Where a chunk's scales lie in 1 .. 2^15 units they weigh the
+      // probabilities: p vs / v_ref is 65504 at most and no smaller than p.  Where not (`apart`), each slice's product
+      // is taken with the probabilities alone and weighed in fp32.
+      const float v_new = v_hi > kUnits * v_ref ? value_unit(v_ref, v_hi, v_hi * 0x1p-8f) : v_ref;
+      const bool apart = v_lo < v_new || v_hi > kUnits * v_new;
       bool grew = v_new != v_ref;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
           grew |= mx[nt][e] != m[nt][e];
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
-        if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
+        if (v_new != v_ref) v_inv = per_unit(v_new);
         const float fv = v_ref * v_inv;  // of the values summed so far
         v_ref = v_new;
 #pragma unroll
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
         const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
         for (int sl = 0; sl < SL; ++sl) {
-          const float vr = vs[sl] * v_inv;
+          const float vr = apart ? 1.0f : vs[sl] * v_inv;
           const float p0 = ex2(s[sl][nt][0] - m0), p1 = ex2(s[sl][nt][1] - m1);
           const float p2 = ex2(s[sl][nt][2] - m0), p3 = ex2(s[sl][nt][3] - m1);
           l[nt][0] += p0 + p2;
@@ -363,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
             w[k][0] = x.x, w[k][1] = x.y;
           }
         }
+        const float weight = vs[sl] * v_inv;  // where the slices are apart
         if (some_hidden) {
           bool bad = false;
 #pragma unroll
@@ -412,16 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
             }
           }
         }
+        auto products = [&](auto alone) {
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
+          for (int i = 0; i < NW; ++i)
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            uint32_t a0, a1, a2, a3;
-            cvt4(__byte_perm(w[0][i], w[1][i], p ? 0x7362 : 0x5140), a0, a1);
-            cvt4(__byte_perm(w[2][i], w[3][i], p ? 0x7362 : 0x5140), a2, a3);
+            for (int p = 0; p < 2; ++p) {
+              uint32_t a0, a1, a2, a3;
+              cvt4(__byte_perm(w[0][i], w[1][i], p ? 0x7362 : 0x5140), a0, a1);
+              cvt4(__byte_perm(w[2][i], w[3][i], p ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * i + p][nt], a0, a1, a2, a3, pb[sl][nt][0], pb[sl][nt][1]);
-          }
+              for (int nt = 0; nt < NT; ++nt) {
+                float(&sum)[4] = o[2 * i + p][nt];
+                if constexpr (decltype(alone)::value) {
+                  float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma_f16(part, a0, a1, a2, a3, pb[sl][nt][0], pb[sl][nt][1]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) sum[k] = fmaf(part[k], weight, sum[k]);
+                } else {
+                  mma_f16(sum, a0, a1, a2, a3, pb[sl][nt][0], pb[sl][nt][1]);
+                }
+              }
+            }
+        };
+        if (apart)
+          products(std::true_type());
+        else
+          products(std::false_type());
       }
       __syncwarp();  // every lane has read the stage
       fetch();

@@ -36,6 +36,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The unit of a tile's sums of values: a power of two, not far from the value scales that its tokens have, since what
+// enters the tensor cores is fp16.  `most`: the largest scale of the tokens that come next; `to`: the unit wanted
+// for it.  A unit only grows, and by at most 2^100 unless `most` is out of fp32's reach under it, so that sums
+// under the old one keep their bits whatever becomes of the new tokens; 2^19 is enough for any scale.
+__device__ __forceinline__ float value_unit(float unit, float most, float to) {
+  float u = fminf(to, 0x1p19f);
+  if (unit > 0.0f) u = fmaxf(fmaxf(unit, fminf(u, unit * 0x1p100f)), most * 0x1p-100f);
+  return __uint_as_float(__float_as_uint(u) & 0xFF800000u);
+}
+// 1 / unit, exact (2^-119 .. 2^125 for a unit of 2^-108 .. 2^19); anything finite for 0
+__device__ __forceinline__ float per_unit(float unit) { return __uint_as_float((254u << 23) - __float_as_uint(unit)); }
+
 __device__ __forceinline__ void cp_async4(float* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
@@ -45,7 +57,7 @@ struct Tile {
   int b, h, rt;
   int len, m, row0;    // the sequence's tokens, queries, first row of q
   int chunk0, chunks;  // its run of chunks (at least one, so that every tile is written)
-  int hi;              // tokens from here on are seen by no row
+  int lo, hi;          // tokens before lo, and from hi on, are seen by no row
 };
 
 __device__ __forceinline__ void sequence(const AttnParams& a, int b, int& len, int& m, int& row0) {
@@ -70,6 +82,7 @@ __device__ __forceinline__ void set_rows(const AttnParams& a, int G, Tile& t) {
   int hi = t.len, lo = 0;
   if (a.causal) hi = max(0, min(t.len, t.len - t.m + min(t.m - 1, by_group(t.rt * R + R - 1, G)) + 1));
   if (a.window > 0) lo = int(max(int64_t(0), int64_t(t.len) - t.m + by_group(t.rt * R, G) - a.window + 1));
+  t.lo = lo;
   t.hi = hi;
   t.chunk0 = lo / CH;
   t.chunks = max(1, (hi + CH - 1) / CH - t.chunk0);

@@ -25,6 +25,10 @@
 // leave.  bf16 has 8 bits and fp16 11, an e4m3 number takes off at least 4 of them, so the
 // sum is exact but for what lies below e4m3's smallest step, 2^-10 or 2^-17 of the row's
 // largest.  Two terms take as long as one fp16 product, and the keys need no conversion.
+// The value scales weigh the probabilities, in units 2^5 below the first block's largest: up to 2^7 units
+// fp16 holds the weighted probabilities with no fewer bits than the plain ones; where a larger scale comes the
+// unit is raised.  A block with a smaller one takes bf16 instead, whose range holds every scale, on
+// the values' side, and its probabilities as sums of two numbers in two products.
 //
 // Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 329 us,
 // 713 TFLOP/s; 512 queries over 8000: 97 us, 670 TFLOP/s.  A block takes a CTA about 2600
@@ -59,7 +63,7 @@ struct RowsCfg {
   static constexpr int kV = kQ + TERMS * R * D;       // 2 x [CH / 64][D][64 tokens]
   static constexpr int kRawK = kV + 2 * CH * D * 2;   // 2 x e4m3 as in the cache
   static constexpr int kRawV = kRawK + 2 * kRawBytes;
-  static constexpr int kNan = kRawV + kRawBytes;      // 4 x [CH tokens][4 words]: elements of a token that are NaN
+  static constexpr int kNan = kRawV + 2 * kRawBytes;    // 4 x [CH tokens][4 words]: elements of a token that are NaN
   static constexpr int kScales = kNan + 4 * CH * 16;  // 8 x [SL] (key, value) scales
   static constexpr int kBars = kScales + 8 * SL * 8;
   static constexpr int kXch = kBars + 256;            // between a row's two threads: maxima [2][2][128], sums, query maxima
@@ -71,6 +75,8 @@ struct RowsCfg {
 
 constexpr float kLeast = 1.0e-37f;  // of a score's factor: not 0, hidden scores are -inf times it
 constexpr float kGrow = 8.0f;  // log2 of what a maximum may grow by before O is rescaled
+// Value scales, in units of the tile's sums, of up to 2^7 weigh the probabilities: 2^15 at most, and none loses bits.
+constexpr float kUnits = 128.0f;
 
 // fp32 sums of fp16 (kind::f16) or of e4m3 (kind::f8f6f4): type codes 0 both
 __host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
@@ -147,6 +153,11 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {  // saturating, NaN stays NaN
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -159,6 +170,52 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uin
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// For a block whose value scales are apart, kept out of the loops that every block goes through: calls in them keep
+// the compiler from taking the next loads ahead, and products take a longer way (4 prompts of 1024 queries
+// over 4000 tokens: 366 us, 322 so).
+// A row's probabilities as sums of two bf16 numbers each, exactly: fp16 has 11 bits.
+template <int kCols>
+__device__ __noinline__ void split_probabilities(uint32_t s_at) {
+#pragma unroll 1
+  for (int i = 0; i < kCols / 2; i += 16) {
+    uint32_t w[16], rest[16];
+    tc::tmem_ld_16cols(s_at + i, w);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      w[j] = pack_bf16(p.x, p.y);
+      rest[j] = pack_bf16(p.x - __uint_as_float(w[j] << 16), p.y - __uint_as_float(w[j] & 0xFFFF0000u));
+    }
+    tmem_st_16cols(s_at + i, w);
+    tmem_st_16cols(s_at + kCols / 2 + i, rest);
+  }
+}
+
+// A lane's words of converted values in bf16, whose range holds them under every scale.
+template <int CH, int D>
+__device__ __noinline__ void widen_values(uint8_t* v_at, const float2* scales, int w, int lane) {
+#pragma unroll 1
+  for (int i = 0; i < CH / 64 * (D / 64) * 16; ++i) {
+    const int atom = i / (D / 4), row = w * (D / 4) + i % (D / 4);
+    const float weight = scales[4 * atom + (lane >> 3)].y;
+    uint32_t* at = reinterpret_cast<uint32_t*>(v_at + atom * (D * 128) + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(at));
+    *at = pack_bf16(f.x * weight, f.y * weight);
+  }
+}
+
+// Both terms of the probabilities times the values.
+template <int CH, int R, int D>
+__device__ __noinline__ void products_apart(uint32_t o_at, uint32_t p_at, uint64_t v_desc, bool fresh) {
+  constexpr int N = CH / 16;
+#pragma unroll 1
+  for (int i = 0; i < 2 * N; ++i) {
+    const int k = i % N;
+    mma_a_tmem(o_at, p_at + CH / 2 * (k / (N / 2)) + CH / 4 * (i / N) + 8 * (k % (N / 2)),
+               v_desc + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), tc::idesc_bf16(R, D, false), !fresh || i > 0);
+  }
 }
 
 template <typename T, int D>
@@ -176,7 +233,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
   // Barriers of the pipeline.  Those with two or more places take blocks in turn, so that no
   // waiter is ever two phases behind.
   uint64_t* raw_k = bars;                                   // [2] key bytes landed
-  uint64_t *raw_v = bars + 4, *raw_v_free = bars + 5;       // value bytes landed, read
+  uint64_t *raw_v = bars + 2, *raw_v_free = bars + 4;       // [2] value bytes landed, read
   uint64_t* v_full = bars + 7;                              // [2] values converted
   uint64_t* s_full = bars + 9;                              // [2] scores done (the keys' place is free)
   uint64_t* p_full = bars + 11;                             // [2] probabilities written
@@ -189,10 +246,11 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
   int* last_flag = abort_flag + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(abort_flag + 2);
   int* nan_block = abort_flag + 4;  // [4] 1 + number of the block whose NaN masks are valid
-  float* v_max = reinterpret_cast<float*>(misc + 24);  // [8] the largest value scale of a block
+  // [8] the unit of the values' sums from a block on, negative where the block's value scales are apart (kUnits)
+  volatile float* v_unit = reinterpret_cast<float*>(misc + 24);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 25; ++i)  // arrivals: of the converting warps, of the softmax warps, or one
-      tc::mbar_init(bars + i, i == 5 || i == 7 || i == 8 ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
+      tc::mbar_init(bars + i, i == 4 || i == 5 || i == 7 || i == 8 ? 4 : i == 11 || i == 12 || i == 15 ? 8 : 1);
     tc::fence_barrier_init();
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_block[i] = 0;
@@ -294,7 +352,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
       const int last_row = min(t.m - 1, (t.rt * R + R - 1) / G);
       const int all_lo = a.window > 0 ? int(max(int64_t(0), t.len - t.m + last_row - a.window + 1)) : 0;
 
-      float m = -INFINITY, l = 0.0f, v_ref = 0.0f, v_inv = 0.0f;  // l: of this thread's scores
+      float m = -INFINITY, l = 0.0f, v_ref = 0.0f;  // l: of this thread's scores; v_ref: the unit of O
       // elements half * D / 2 on of the row that a NaN value reaches
       uint32_t nan_row[D / 64];
 #pragma unroll
@@ -324,7 +382,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         float kf[SL / 2];
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) kf[i] = fmaxf(sc[i].x * row_scale, kLeast);
-        const float v_new = fmaxf(v_ref, v_max[g & 7]);
+        const float unit = v_unit[g & 7], v_new = fabsf(unit);
         float s[kCols];  // products; hidden ones -inf
         tmem_ld_64cols(s_at, reinterpret_cast<uint32_t(&)[64]>(s));
         // Below, a score is not rounded before the maximum, which is, is taken off; from 2^24 on it could lie far
@@ -359,8 +417,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
           const float f = grow ? ex2(m - mx) : 1.0f;  // 0 for a row's first scores
           if (grow) m = mx;
           l *= f;
-          if (v_new != v_ref) v_inv = __fdiv_rn(1.0f, v_new);
-          const float fo = f * (v_ref * v_inv);
+          const float fo = v_new != v_ref ? f * (v_ref * per_unit(v_new)) : f;
           v_ref = v_new;
           if (!first) {  // O is these threads' once the block before has been added
             wait(o_done + ((g - 1) & 1), (g - 1) >> 1);
@@ -381,22 +438,26 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         uint64_t sum[2] = {0, 0};  // of even and odd scores, in turn
 #pragma unroll
         for (int i = 0; i < SL / 2; ++i) {
-          const float vr = sc[i].y * v_inv;
+          const float vr = unit < 0.0f ? 1.0f : sc[i].y;
           const uint64_t k2 = pack2(kf[i], kf[i]), vr2 = pack2(vr, vr);
           uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float2 e = unpack2(fma2(pack2(s[16 * i + 2 * j], s[16 * i + 2 * j + 1]), k2, base2));
-            const uint64_t p = pack2(ex2(e.x), ex2(e.y));
-            sum[j & 1] = add2(sum[j & 1], p);
-            const float2 weight = unpack2(mul2(p, vr2));
-            w[j] = pack_f16(weight.x, weight.y);
+            const uint64_t p2 = pack2(ex2(e.x), ex2(e.y));
+            sum[j & 1] = add2(sum[j & 1], p2);
+            const float2 p = unpack2(mul2(p2, vr2));
+            w[j] = pack_f16(p.x, p.y);
           }
           tmem_st_8cols(s_at + 8 * i, w);  // over scores that this thread has read
         }
         const float2 both = unpack2(add2(sum[0], sum[1]));
         l += both.x + both.y;
         tc::tmem_wait_st();
+        if (unit < 0.0f) {
+          split_probabilities<kCols>(s_at);
+          tc::tmem_wait_st();
+        }
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + (g & 1));
@@ -510,7 +571,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
     for (int i = threadIdx.x - 256; i < 4 * CH; i += 128) reinterpret_cast<uint4*>(smem + C::kNan)[i] = make_uint4(0, 0, 0, 0);
     tc::named_bar_sync(2, 128);
     auto convert_v = [&](int g, int behind) {  // behind: tokens of the block before what no row sees
-      bool ok = wait(raw_v, g);
+      bool ok = wait(raw_v + (g & 1), g >> 1);
       if (ok && g > 1) ok = wait(o_done + (g & 1), (g - 2) >> 1);
       if (!__all_sync(0xFFFFFFFFu, ok)) return false;
       uint32_t had = 0;
@@ -521,7 +582,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int tok = 64 * atom + 2 * lane + k;
-          const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kRawV + tok * D +
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + C::kRawV + (g & 1) * C::kRawBytes + tok * D +
                                                           ((p ^ (D == 128 ? tok & 7 : (tok >> 1) & 3)) << 4));
           const bool in = tok < behind;  // behind them anything may lie
           x[k][0] = in ? v.x : 0, x[k][1] = in ? v.y : 0, x[k][2] = in ? v.z : 0, x[k][3] = in ? v.w : 0;
@@ -555,13 +616,15 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
             *reinterpret_cast<uint32_t*>(dst + (4 * j + k) * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
         }
       }
+      if (!__all_sync(0xFFFFFFFFu, wait(scales_full + (g & 7), g >> 3))) return false;
+      if (v_unit[g & 7] < 0.0f) widen_values<CH, D>(smem + C::kV + (g & 1) * (CH * D * 2), scales + SL * (g & 7), w, lane);
       dirty = (dirty & ~(1u << (g & 3))) | uint32_t(had != 0) << (g & 3);
       if (had) nan_block[g & 3] = g + 1;
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         tc::mbar_arrive(v_full + (g & 1));
-        tc::mbar_arrive(raw_v_free);
+        tc::mbar_arrive(raw_v_free + (g & 1));
       }
       return true;
     };
@@ -580,14 +643,24 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         const int tok = (t.chunk0 + c) * CH + 16 * (lane & (SL - 1));
         return lane < SL && tok < t.hi ? a.block_table[t.b * a.max_pages + (tok >> P.page_shift)] : -1;
       };
-      int next = page_of(cur.c);
+      auto in_pool = [&](int phys) { return phys >= 0 && phys < a.n_pages; };
+      // of a lane's slice: (key, value) scales; (1, 0) where no row sees it or it reads as zeros
+      auto scales_of = [&](int c, int phys) {
+        const int tok = (t.chunk0 + c) * CH + 16 * (lane & (SL - 1));
+        if (lane >= SL || tok >= t.hi || !in_pool(phys)) return make_float2(1.0f, 0.0f);
+        const int blk = phys * a.kv_heads + t.h;
+        return make_float2(a.k_scale[blk], tok + 16 > t.lo ? a.v_scale[blk] : 0.0f);
+      };
+      // page ids are read two blocks ahead, scales one: their latency is hidden behind the waits
+      int phys = page_of(cur.c), next = cur.c + 1 < cur.c_end ? page_of(cur.c + 1) : -1;
+      float2 sc = scales_of(cur.c, phys);
+      float unit = 0.0f, inverse = 0.0f;  // of the tile's values, and its reciprocal
       for (int c = cur.c; c < cur.c_end; ++c, ++g) {
-        const int t0 = (t.chunk0 + c) * CH, tok = t0 + 16 * (lane & (SL - 1)), phys = next;
-        if (c + 1 < cur.c_end) next = page_of(c + 1);
+        const int t0 = (t.chunk0 + c) * CH, tok = t0 + 16 * (lane & (SL - 1));
         const int box = 1 << P.box_shift;
         const int n_box = max(min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift), 0);
         const uint32_t bytes = uint32_t(n_box * D) << P.box_shift;
-        const bool in = phys >= 0 && phys < a.n_pages, wanted = lane < SL && tok < t.hi;
+        const bool in = in_pool(phys), wanted = lane < SL && tok < t.hi;
         if (wanted && !in) set_status(a.status, PATCH_DEV_BOUNDS);
         const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
         const bool leads = wanted && (16 * lane & (box - 1)) == 0;
@@ -604,25 +677,35 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         ok = g < 2 || wait(s_full + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.k_map, raw_k_at + (g & 1) * C::kRawBytes, raw_k + (g & 1));
-        float2 sc = make_float2(1.0f, 0.0f);  // no row sees the slice, or it reads as zeros
-        if (wanted && in) sc = make_float2(a.k_scale[blk], a.v_scale[blk]);
-        ok = g < 1 || wait(raw_v_free, g - 1);
+        ok = g < 2 || wait(raw_v_free + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        issue(&P.v_map, raw_v_at, raw_v);
-        if (lane < SL) scales[SL * (g & 7) + lane] = sc;
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sc.y));  // none is negative
-        if (lane == 0) v_max[g & 7] = __uint_as_float(most);
+        issue(&P.v_map, raw_v_at + (g & 1) * C::kRawBytes, raw_v + (g & 1));
+        // the largest value scale and the smallest but 0 (none is negative: their order is that of their bits)
+        const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sc.y)));
+        const float least = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(sc.y > 0.0f ? sc.y : INFINITY)));
+        if (most > kUnits * unit) {
+          unit = value_unit(unit, most, most * 0x1p-5f);
+          inverse = per_unit(unit);
+        }
+        if (lane < SL) scales[SL * (g & 7) + lane] = make_float2(sc.x, sc.y * inverse);
+        if (lane == 0) v_unit[g & 7] = most > kUnits * unit || least < unit ? -unit : unit;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(scales_full + (g & 7));
+        if (c + 1 < cur.c_end) {
+          phys = next;
+          sc = scales_of(c + 1, phys);
+          if (c + 2 < cur.c_end) next = page_of(c + 2);
+        }
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
     if (!ok) {  // after a timeout: let the copies in flight land (one of each ring place at most is not awaited yet)
       for (int i = 0; i < 2; ++i) {
         const int last = g - 1 - i;
-        if (last >= 0) tc::wait_bounded(raw_k + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
+        if (last < 0) break;
+        tc::wait_bounded(raw_k + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
+        tc::wait_bounded(raw_v + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
       }
-      if (g > 0) tc::wait_bounded(raw_v, (g - 1) & 1, abort_flag, P.limit_ns, a.status, true);
     }
   } else if (lane == 0) {
     // ================= the products
@@ -637,11 +720,15 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
       if (!wait(v_full + (g & 1), g >> 1) || !wait(p_full + (g & 1), g >> 1)) return false;
       tc::tc_fence_after();
       const bool fresh = first_bits >> (g & 31) & 1;
+      if (v_unit[g & 7] < 0.0f) {
+        products_apart<CH, R, D>(tmem + C::kO, tmem + (g & 1) * CH, v_desc + (g & 1) * (CH * D * 2 / 16), fresh);
+      } else {
 #pragma unroll
-      for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P (in its half), 32 bytes of a row of V
-        mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + kCols * (k / (SL / 2)) + 8 * (k % (SL / 2)),
-                   v_desc + (g & 1) * (CH * D * 2 / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), idesc_f32(R, D),
-                   !fresh || k > 0);
+        for (int k = 0; k < CH / 16; ++k)  // 16 tokens: 8 columns of P (in its half), 32 bytes of a row of V
+          mma_a_tmem(tmem + C::kO, tmem + (g & 1) * CH + kCols * (k / (SL / 2)) + 8 * (k % (SL / 2)),
+                     v_desc + (g & 1) * (CH * D * 2 / 16) + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), idesc_f32(R, D),
+                     !fresh || k > 0);
+      }
       tc::tc_commit(o_done + (g & 1));
       return true;
     };
