@@ -842,7 +842,7 @@ PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_head
  * cores as fp16, and so does q, divided by a power of two of its own row first
  * so that no finite value overflows; with 64 query rows or more for a sequence
  * and key/value head on average, q enters as a sum of two (bf16) or three (fp16)
- * e4m3 numbers instead, exact but for at most 2^-17 of the row's largest element.
+ * e4m3 numbers instead, exact but for at most 2^-17 of the row's largest element (or 2^-136).
  * A probability below 2^-14 of its row's largest is off by up to 2^-25 of that.  A page's
  * value scale takes no bits from another page's values, however far apart the two are.
  *   q, out     n_tokens rows of heads (q->heads a multiple of kv_heads, at most

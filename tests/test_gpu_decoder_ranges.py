@@ -130,3 +130,37 @@ def test_attn_values_under_the_least_and_largest_scales(tile):
         return f
     for value in (2.0**-100, 2.0**-60, 2.0**40, 2.0**100):
         attend(tile, 64, BF16, alone(value), seed=6)
+
+
+@pytest.mark.parametrize("m,H", [(1, 1), (3, 4), (90, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_queries_at_the_ends_of_bf16(m, H, D):
+    """One token in view, so lse is its score: rows whose largest element is bf16's largest, 2^127, 2^126, its least
+    normal and its least number at all.  A row is divided by a power of two and then off by 2^-25 (fp16) or, in
+    128-row tiles, 2^-17 of its largest element, or there by 2^-136 if that is more; D fp32 additions beside."""
+    g = gen(41)
+    tops = [torch.finfo(BF16).max, 2.0**127, 2.0**126, 2.0**-126, 2.0**-133, -torch.finfo(BF16).max]
+    B = len(tops)
+    cache = random_cache(B, 1, 16, D, g)
+    q = torch.zeros(B * m, H, D, dtype=BF16, device="cuda")
+    for b, top in enumerate(tops):
+        x = torch.rand(m, H, D, generator=g, device="cuda").double() - 0.5
+        x[..., 3] = 1.0
+        q[b * m : (b + 1) * m] = (x * top).to(BF16)
+        cache.k_scale[b] = 2.0**100 if abs(top) < 1 else 2.0**-4
+    bt = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    cu = i32([m * b for b in range(B + 1)])
+    scales = [2.0**-122 if abs(t) > 1 else 2.0**22 for t in tops]
+    for scale in sorted(set(scales)):
+        st = tsg.new_status()
+        out, lse = tsg.patch_attn_kv8(q, cache, bt, i32([1] * B), cu, scale, False, want_lse=True, status=st)
+        assert tsg.patch_read_status(st) == (0, 0)
+        for b in [b for b in range(B) if scales[b] == scale]:
+            rows = slice(b * m, (b + 1) * m)
+            k = cache.k[b, 0, 0].double() * cache.k_scale[b, 0].double()
+            x = q[rows].double()
+            bound = scale * ((2.0**-16 if m > 64 else 2.0**-24) * x.abs().amax(-1) * k.abs().sum()
+                             + 2.0**-136 * k.abs().sum() + 3 * (D + 2) * 2.0**-24 * (x.abs() @ k.abs())) + 1e-30
+            within(lse[rows], (x @ k) * scale, bound, f"lse {tops[b]}")
+            v = (cache.v[b, 0, 0].double() * cache.v_scale[b, 0].double()).expand(m, H, D)
+            within(out[rows], v, 2.0**-8 * v.abs() + 1e-30, f"out {tops[b]}")
