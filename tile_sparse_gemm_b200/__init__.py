@@ -138,6 +138,21 @@ def _check(code: int, what: str):
         raise PatchError(code, what)
 
 
+def _new(shape, dtype: torch.dtype, device, stream=None, zero: bool = False) -> torch.Tensor:
+    """What a call on `stream` (None: the current one) makes for itself, allocated and zero-filled there: memory that
+    the current stream may still use is not handed out, and the zeros are written before the call's kernels run.  The
+    caller's stream is recorded, so that a result may be used and dropped there (once it has waited for `stream`)."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if not zero:  # a result; workspaces end with the call
+        t.record_stream(caller)
+    return t
+
+
 def _stream(stream=None) -> ctypes.c_void_p:
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)

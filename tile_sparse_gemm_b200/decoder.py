@@ -5,8 +5,9 @@ Thin binding over the C ABI (include/patch.h), like the rest of the package: it
 checks and marshals arguments, every step runs in the library's sm_100a
 kernels.  The calls run on the tensors' own device and on `stream` (default:
 that device's current stream), launch only libpatch kernels, allocate only the
-outputs they are not given, never synchronise and can be captured in a CUDA
-graph.  A device status word is optional: `status=new_status()` collects what
+outputs and workspace they are not given (on that stream), never synchronise and
+can be captured in a CUDA graph.  Who passes a `stream` orders it after the inputs'
+writers and before the results' readers, and keeps the inputs until it is done.  A device status word is optional: `status=new_status()` collects what
 the kernels report (patch_read_status).
 
 The calls of a decode step take less time on the device than their checks take
@@ -22,7 +23,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import PatchError, _check, lib
+from . import PatchError, _check, _new, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # PATCH_DTYPE_*
 LAYOUTS = {"half": 0, "interleaved": 1}                           # PATCH_ROPE_HALF / PATCH_ROPE_INTERLEAVED
@@ -150,10 +151,10 @@ def _heads(t: torch.Tensor, name: str, device, dtype, shape=None) -> _Heads:
     return _Heads(t.data_ptr(), t.shape[1], tok, head)
 
 
-def _new_heads(t: torch.Tensor) -> tuple[torch.Tensor, _Heads]:
+def _new_heads(t: torch.Tensor, stream) -> tuple[torch.Tensor, _Heads]:
     """A contiguous output of t's shape, type and device."""
     T, H, D = t.shape
-    out = torch.empty((T, H, D), dtype=t.dtype, device=t.device)
+    out = _new((T, H, D), t.dtype, t.device, stream)
     return out, _Heads(out.data_ptr(), H, H * D, D)
 
 
@@ -182,7 +183,7 @@ def patch_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: s
     cfg = _RopeConfig(ROPE_SCALINGS[scaling], 0, base, factor, original_positions, low_freq, high_freq, amplitude)
     if n_pos < 1 or rot_dim < 2:
         raise PatchError(2, "patch_rope_table")
-    table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    table = _new((n_pos, rot_dim // 2, 2), torch.float32, device, stream)
     _call("patch_rope_table", table.device, stream, n_pos, rot_dim, _byref(cfg), table.data_ptr())
     return table
 
@@ -225,14 +226,14 @@ def patch_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     tab, n_pos, rot = _table(table, dev)
     pos = _tensor(positions, "positions", dev, torch.int32, (T,))
     if q_out is None:
-        q_out, ho = _new_heads(q)
+        q_out, ho = _new_heads(q, stream)
     else:
         ho = _heads(q_out, "q_out", dev, dtype, q.shape)
     hk = hko = None
     if k is not None:
         hk = _byref(_heads(k, "k", dev, dtype, (T, k.shape[1], D)))
         if k_out is None:
-            k_out, hko = _new_heads(k)
+            k_out, hko = _new_heads(k, stream)
         else:
             hko = _heads(k_out, "k_out", dev, dtype, k.shape)
         hko = _byref(hko)
@@ -355,12 +356,12 @@ def patch_attn_kv8(q: torch.Tensor, cache: KvCache8, block_table: torch.Tensor, 
     lens = _tensor(kv_lens, "kv_lens", dev, torch.int32, (batch,))
     cu = None if cu_q is None else _tensor(cu_q, "cu_q", dev, torch.int32, (batch + 1,))
     if out is None:
-        out, ho = _new_heads(q)
+        out, ho = _new_heads(q, stream)
     else:
         ho = _heads(out, "out", dev, dtype, shape)
-    lse = torch.empty((T, H), dtype=torch.float32, device=dev) if want_lse else None
+    lse = _new((T, H), torch.float32, dev, stream) if want_lse else None
     if workspace is None:
-        workspace = torch.zeros(max(patch_attn_kv8_workspace_size(T, batch, H, cache), 16), dtype=torch.uint8, device=dev)
+        workspace = _new((max(patch_attn_kv8_workspace_size(T, batch, H, cache), 16),), torch.uint8, dev, stream, zero=True)
     ws = _tensor(workspace, "workspace", dev, torch.uint8)
     _call("patch_attn_kv8", dev, stream, _byref(hq), T, dt, _byref(c), bt, max_pages, lens, cu, batch,
           1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, _byref(ho),
@@ -415,8 +416,7 @@ def patch_quantize4(W: torch.Tensor, group: int = 128, scale_dtype: torch.dtype 
         raise ValueError(f"scale_dtype {scale_dtype}, expected torch.bfloat16 or torch.float16")
     dev = _cuda(W, "W")
     p = _tensor(W, "W", dev, W.dtype)
-    w4 = Weight4(torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
-                 torch.empty((N, K // group), dtype=scale_dtype, device=dev), group)
+    w4 = Weight4(_new((N, K // 2), torch.uint8, dev, stream), _new((N, K // group), scale_dtype, dev, stream), group)
     st = w4.struct()
     _call("patch_quantize4", dev, stream, p, _dtype(W, "W", DTYPES), _byref(st))
     return w4
@@ -440,7 +440,7 @@ def patch_gemm4(X: torch.Tensor, weight: Weight4, Y: torch.Tensor | None = None,
     dt = _dtype(X, "X")
     x = _tensor(X, "X", dev, dtype)
     if Y is None:
-        Y = torch.empty((M, n), dtype=dtype, device=dev)
+        Y = _new((M, n), dtype, dev, stream)
     _call("patch_gemm4", dev, stream, x, M, dt, _byref(st), _tensor(Y, "Y", dev, dtype, (M, n)),
           _status(status, dev))
     return Y
