@@ -58,3 +58,29 @@ def test_results_outlive_their_last_use_on_the_callers_stream():
     other = [tsg.patch_gemm4(-x, w, stream=s) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and all(torch.equal(o, -want) for o in other)
+
+
+def test_hybrid_decode_gemm_without_a_workspace():
+    """The decode kernel's counters and sums lie in a workspace that must be zero before it runs."""
+    import oracle
+    import synth_inputs as si
+    from _util import bits_of, check_gemm, to_dev, to_dev_bf16
+
+    N, K, M = 2048, 2048, 16
+    w, bm = si.gen_w(N, K, 3, 1), si.tiles_exact(N, K, 0.5, 3, 1)
+    ids = si.patterns_top2(w)
+    pw = tsg.patch_pack(to_dev_bf16(w), to_dev(bm), to_dev(ids), int(bm.sum()))
+    x = si.gen_x(M, K, 3, 2)
+    xd = to_dev_bf16(x)
+    want = oracle.hybrid_gemm(x, w, bm, ids)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for call in (lambda: tsg.patch_gemm(xd, pw, stream=s), lambda: tsg.patch_gemm_chain([(xd, pw, None, False)], stream=s)[0],
+                 lambda: tsg.patch_gemm_group([(xd, pw, None)], stream=s)[0]):
+        busy_and_dirty(tsg.patch_gemm_workspace_size(M, pw))
+        y = call()
+        s.synchronize()
+        with torch.cuda.stream(s):
+            got = bits_of(y)
+        check_gemm(got, want, "another stream")
+        torch.cuda.synchronize()

@@ -69,3 +69,36 @@ def test_decoder_calls(log):
     log.clear()
     tsg.patch_quantize4(torch.ones(6, 64), 64, stream=s)
     check(log, s, 2)
+
+
+class FakeLib:
+    """Every entry point returns PATCH_OK; those that take a stream are launches on it."""
+
+    def __init__(self, events):
+        self.events = events
+
+    def __getattr__(self, name):
+        def call(*a):
+            if not name.endswith("_size") and not name.endswith("_sizes"):
+                at = next(x for x in a if getattr(x, "value", None) == FakeStream.cuda_stream)
+                self.events.append(("launch", at.value))
+            return 0
+        return call
+
+
+def test_hybrid_calls(log, monkeypatch):
+    s = FakeStream()
+    monkeypatch.setattr(tsg, "lib", lambda: FakeLib(log))
+    monkeypatch.setattr(tsg, "_dev", lambda t, name: None)
+    N = K = 128
+    u8 = torch.uint8
+    W, x = torch.ones(N, K, dtype=BF16), torch.ones(4, K, dtype=BF16)
+    pw = tsg.PackedWeight(N, K, 0, torch.ones(16, dtype=u8), torch.ones(16, dtype=u8), torch.ones(16, dtype=u8))
+    for call in (lambda: tsg.patch_gemm(x, pw, stream=s), lambda: tsg.patch_gemm_chain([(x, pw, None, False)], stream=s),
+                 lambda: tsg.patch_gemm_group([(x, pw, None)], stream=s), lambda: tsg.patch_gemm_mlp(x, pw, pw, stream=s),
+                 lambda: tsg.patch_check_weight(pw, stream=s)):
+        log.clear()
+        call()
+        made = [e[1] for e in log if e[0] in ("empty", "zeros")]
+        assert made and all(m is s for m in made), log
+        assert log[-1] == ("launch", FakeStream.cuda_stream), log

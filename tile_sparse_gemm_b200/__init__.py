@@ -138,17 +138,19 @@ def _check(code: int, what: str):
         raise PatchError(code, what)
 
 
-def _new(shape, dtype: torch.dtype, device, stream=None, zero: bool = False) -> torch.Tensor:
+def _new(shape, dtype: torch.dtype, device, stream=None, zero: bool = False,
+         kept: bool | None = None) -> torch.Tensor:
     """What a call on `stream` (None: the current one) makes for itself, allocated and zero-filled there: memory that
-    the current stream may still use is not handed out, and the zeros are written before the call's kernels run.  The
-    caller's stream is recorded, so that a result may be used and dropped there (once it has waited for `stream`)."""
+    the current stream may still use is not handed out, and the zeros are written before the call's kernels run.  For
+    what outlives the call (kept; unless said, all but what is zeroed) the caller's stream is recorded, so that a result
+    may be used and dropped there (once it has waited for `stream`)."""
     make = torch.zeros if zero else torch.empty
     if stream is None:
         return make(shape, dtype=dtype, device=device)
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         t = make(shape, dtype=dtype, device=device)
-    if not zero:  # a result; workspaces end with the call
+    if kept or (kept is None and not zero):
         t.record_stream(caller)
     return t
 
@@ -240,10 +242,10 @@ def patch_hard_mask(W: torch.Tensor | None, tile_logits: torch.Tensor, pattern_l
     N, K4, _ = pattern_logits.shape
     K = 4 * K4
     dev = pattern_logits.device
-    status = new_status(dev) if status is None else status
-    wm = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if want_masked else None
-    bitmap = torch.empty((N // TILE, K // TILE), dtype=torch.uint8, device=dev)
-    pid = torch.empty((N, K // 4), dtype=torch.uint8, device=dev)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
+    wm = _new((N, K), torch.bfloat16, dev, stream) if want_masked else None
+    bitmap = _new((N // TILE, K // TILE), torch.uint8, dev, stream)
+    pid = _new((N, K // 4), torch.uint8, dev, stream)
     _check(lib().patch_hard_mask(_dev(W, "W"), N, K, _dev(tile_logits, "tile_logits"),
                                  _dev(pattern_logits, "pattern_logits"), _dev(wm, "W_masked"),
                                  _dev(bitmap, "bitmap"), _dev(pid, "pat_id"), _dev(status, "status"),
@@ -260,11 +262,11 @@ def patch_hard_mask_tiles(W: torch.Tensor | None, tile_logits: torch.Tensor, pat
     K = 4 * K4
     b = int(mask_tile)
     dev = pattern_logits.device
-    status = new_status(dev) if status is None else status
-    wm = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if want_masked else None
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
+    wm = _new((N, K), torch.bfloat16, dev, stream) if want_masked else None
     shape = (N // b, K // b) if b in MASK_TILES else (1,)  # the library rejects other sizes
-    bitmap = torch.empty(shape, dtype=torch.uint8, device=dev)
-    pid = torch.empty((N, K // 4), dtype=torch.uint8, device=dev)
+    bitmap = _new(shape, torch.uint8, dev, stream)
+    pid = _new((N, K // 4), torch.uint8, dev, stream)
     _check(lib().patch_hard_mask_tiles(_dev(W, "W"), N, K, b, _dev(tile_logits, "tile_logits"),
                                        _dev(pattern_logits, "pattern_logits"), _dev(wm, "W_masked"),
                                        _dev(bitmap, "bitmap"), _dev(pid, "pat_id"), _dev(status, "status"),
@@ -277,8 +279,8 @@ def patch_exec_tiles(bitmap: torch.Tensor, N: int, K: int, mask_tile: int,
     """128 x 128 execution tiles of a b x b mask bitmap (sparse only where every
     mask tile inside is sparse): (exec u8 [N/128][K/128], n_sparse int64 [1]), on the device."""
     dev = bitmap.device
-    ex = torch.empty((N // TILE, K // TILE), dtype=torch.uint8, device=dev)
-    n_sparse = torch.empty(1, dtype=torch.int64, device=dev)
+    ex = _new((N // TILE, K // TILE), torch.uint8, dev, stream)
+    n_sparse = _new(1, torch.int64, dev, stream)
     _check(lib().patch_exec_tiles(_dev(bitmap, "bitmap"), N, K, int(mask_tile), _dev(ex, "exec"),
                                   _dev(n_sparse, "n_sparse"), _stream(stream)), "patch_exec_tiles")
     return ex, n_sparse
@@ -292,10 +294,10 @@ def patch_pack(W: torch.Tensor, bitmap: torch.Tensor, pat_id: torch.Tensor, n_sp
         n_sparse = int(torch.count_nonzero(bitmap).item())
     vb, mb, db = patch_pack_sizes(N, K, n_sparse)
     dev = W.device
-    status = new_status(dev) if status is None else status
-    values = torch.empty(vb, dtype=torch.uint8, device=dev)
-    meta = torch.empty(mb, dtype=torch.uint8, device=dev)
-    desc = torch.empty(db, dtype=torch.uint8, device=dev)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
+    values = _new(vb, torch.uint8, dev, stream)
+    meta = _new(mb, torch.uint8, dev, stream)
+    desc = _new(db, torch.uint8, dev, stream)
     _check(lib().patch_pack(_dev(W, "W"), N, K, _dev(bitmap, "bitmap"), _dev(pat_id, "pat_id"), n_sparse,
                             _dev(values, "values"), _dev(meta, "meta") if mb else None, _dev(desc, "desc"),
                             _dev(status, "status"), _stream(stream)), "patch_pack")
@@ -308,8 +310,8 @@ def patch_soft_mask(W: torch.Tensor, tile_logits: torch.Tensor, pattern_logits: 
     """Training-time hybrid mask: (W_soft bf16 [N][K], M fp32 [N][K] or None)."""
     N, K = W.shape
     dev = W.device
-    w_soft = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    mask = torch.empty((N, K), dtype=torch.float32, device=dev) if want_mask else None
+    w_soft = _new((N, K), torch.bfloat16, dev, stream)
+    mask = _new((N, K), torch.float32, dev, stream) if want_mask else None
     _check(lib().patch_soft_mask(_dev(W, "W"), N, K, _dev(tile_logits, "tile_logits"),
                                  _dev(tile_noise, "tile_noise"), _dev(pattern_logits, "pattern_logits"),
                                  _dev(pattern_noise, "pattern_noise"), float(tau), _dev(w_soft, "W_soft"),
@@ -325,8 +327,8 @@ def patch_tile_kinds(tile_logits: torch.Tensor, stream=None) -> tuple[torch.Tens
     if two != 2:
         raise ValueError("tile_logits must be [Tn][Tk][2]")
     dev = tile_logits.device
-    bitmap = torch.empty((Tn, Tk), dtype=torch.uint8, device=dev)
-    n_sparse = torch.empty(1, dtype=torch.int64, device=dev)
+    bitmap = _new((Tn, Tk), torch.uint8, dev, stream)
+    n_sparse = _new(1, torch.int64, dev, stream)
     _check(lib().patch_tile_kinds(_dev(tile_logits, "tile_logits"), Tn * 128, Tk * 128, _dev(bitmap, "bitmap"),
                                   _dev(n_sparse, "n_sparse"), _stream(stream)), "patch_tile_kinds")
     return bitmap, n_sparse
@@ -342,10 +344,10 @@ def patch_pack_from_logits(W: torch.Tensor, bitmap: torch.Tensor, pattern_logits
         n_sparse = int(torch.count_nonzero(bitmap).item())
     vb, mb, db = patch_pack_sizes(N, K, n_sparse)
     dev = W.device
-    status = new_status(dev) if status is None else status
-    values = torch.empty(vb, dtype=torch.uint8, device=dev)
-    meta = torch.empty(mb, dtype=torch.uint8, device=dev)
-    desc = torch.empty(db, dtype=torch.uint8, device=dev)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
+    values = _new(vb, torch.uint8, dev, stream)
+    meta = _new(mb, torch.uint8, dev, stream)
+    desc = _new(db, torch.uint8, dev, stream)
     _check(lib().patch_pack_from_logits(_dev(W, "W"), N, K, _dev(bitmap, "bitmap"),
                                         _dev(pattern_logits, "pattern_logits"), n_sparse, _dev(values, "values"),
                                         _dev(meta, "meta") if mb else None, _dev(desc, "desc"),
@@ -368,12 +370,12 @@ def patch_gemm_ex(X: torch.Tensor, weight: PackedWeight, Y: torch.Tensor | None 
         raise ValueError(f"X has K={K}, weight has K={weight.K}")
     dev = X.device
     if Y is None:
-        Y = torch.empty((M, weight.N), dtype=torch.bfloat16, device=dev)
-    status = new_status(dev) if status is None else status
+        Y = _new((M, weight.N), torch.bfloat16, dev, stream)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
     st = weight.struct()
     if workspace is None:
         need = patch_gemm_workspace_size(M, weight)  # covers every path M can take
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)  # must start zero-filled
+        workspace = _new(max(need, 16), torch.uint8, dev, stream, zero=True)  # must start zero-filled
     _check(lib().patch_gemm_ex(_dev(X, "X"), M, ctypes.byref(st), _dev(Y, "Y"), _dev(workspace, "workspace"),
                                workspace.numel(), _dev(status, "status"), _stream(stream), path, wait_limit_us),
            "patch_gemm")
@@ -397,10 +399,11 @@ class Chain:
     [M][N] (device tensors; Y None allocates it) and after_previous True when
     X is written by an earlier call of the chain (the call then reads X only
     after every earlier call has completed).  The ctypes array of calls and a
-    zero-filled workspace are built once; run() launches the chain on the
-    current stream (capturable in a CUDA graph after one eager run)."""
+    zero-filled workspace are built once, on `stream` (default: the current one);
+    run() launches the chain on its own `stream`, by default the current one
+    (capturable in a CUDA graph after one eager run)."""
 
-    def __init__(self, calls, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    def __init__(self, calls, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
         self.Y = []
         arr = (_ChainCall * len(calls))()
         self._keep = []
@@ -409,7 +412,7 @@ class Chain:
             if K != weight.K:
                 raise ValueError(f"call {j}: X has K={K}, weight has K={weight.K}")
             if Y is None:
-                Y = torch.empty((M, weight.N), dtype=torch.bfloat16, device=X.device)
+                Y = _new((M, weight.N), torch.bfloat16, X.device, stream)
             arr[j] = _ChainCall(_dev(X, "X") if M else None, _dev(Y, "Y") if M else None, weight.struct(), M,
                                 1 if after else 0, 0)
             self.Y.append(Y)
@@ -421,11 +424,11 @@ class Chain:
                "patch_gemm_chain_workspace_size")
         dev = calls[0][0].device if calls else None
         if workspace is None:
-            workspace = torch.zeros(max(b.value, 16), dtype=torch.uint8, device=dev)  # must start zero-filled
+            workspace = _new(max(b.value, 16), torch.uint8, dev, stream, zero=True)  # must start zero-filled
         elif workspace.numel() < b.value:
             raise ValueError(f"workspace of {workspace.numel()} bytes < {b.value} needed")
         self.workspace = workspace
-        self.status = new_status(dev) if status is None else status
+        self.status = _new(1, torch.int32, dev or "cuda", stream, zero=True, kept=True) if status is None else status
 
     @property
     def workspace_bytes(self) -> int:
@@ -441,7 +444,7 @@ class Chain:
 def patch_gemm_chain(calls, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
                      wait_limit_us: int = 0, stream=None) -> list[torch.Tensor]:
     """One launch (per 64 calls) of a sequence of decode GEMMs: see Chain."""
-    return Chain(calls, workspace, status).run(wait_limit_us, stream)
+    return Chain(calls, workspace, status, stream).run(wait_limit_us, stream)
 
 
 class Group:
@@ -449,10 +452,11 @@ class Group:
 
     calls: list of (X, weight, Y) with X bf16 [M][K] and Y bf16 [M][N] device
     tensors (Y None allocates it); no call may write memory another call reads
-    or writes.  The ctypes array of calls is built once; run() launches the
-    group on the current stream (capturable in a CUDA graph after one eager run)."""
+    or writes.  The ctypes array of calls is built once, what it allocates on
+    `stream` (default: the current one); run() launches the group on its own
+    `stream`, by default the current one (capturable in a CUDA graph after one eager run)."""
 
-    def __init__(self, calls, status: torch.Tensor | None = None):
+    def __init__(self, calls, status: torch.Tensor | None = None, stream=None):
         self.Y = []
         arr = (_ChainCall * len(calls))()
         self._keep = []
@@ -461,14 +465,14 @@ class Group:
             if K != weight.K:
                 raise ValueError(f"call {j}: X has K={K}, weight has K={weight.K}")
             if Y is None:
-                Y = torch.empty((M, weight.N), dtype=torch.bfloat16, device=X.device)
+                Y = _new((M, weight.N), torch.bfloat16, X.device, stream)
             arr[j] = _ChainCall(_dev(X, "X") if M else None, _dev(Y, "Y") if M else None, weight.struct(), M, 0, 0)
             self.Y.append(Y)
             self._keep += [X, Y, weight]
         self.calls = arr
         self.n = len(calls)
         dev = calls[0][0].device if calls else None
-        self.status = new_status(dev) if status is None else status
+        self.status = _new(1, torch.int32, dev or "cuda", stream, zero=True, kept=True) if status is None else status
 
     def run(self, wait_limit_us: int = 0, stream=None):
         _check(lib().patch_gemm_group(ctypes.cast(self.calls, ctypes.c_void_p), self.n, _dev(self.status, "status"),
@@ -479,7 +483,7 @@ class Group:
 def patch_gemm_group(calls, status: torch.Tensor | None = None, wait_limit_us: int = 0,
                      stream=None) -> list[torch.Tensor]:
     """One prefill launch (per 32 calls) of independent GEMMs: see Group."""
-    return Group(calls, status).run(wait_limit_us, stream)
+    return Group(calls, status, stream).run(wait_limit_us, stream)
 
 
 def patch_gemm_mlp(X: torch.Tensor, gate: PackedWeight, up: PackedWeight, H: torch.Tensor | None = None,
@@ -491,14 +495,14 @@ def patch_gemm_mlp(X: torch.Tensor, gate: PackedWeight, up: PackedWeight, H: tor
         raise ValueError("X, gate and up shapes disagree")
     dev = X.device
     if H is None:
-        H = torch.empty((M, gate.N), dtype=torch.bfloat16, device=dev)
-    status = new_status(dev) if status is None else status
+        H = _new((M, gate.N), torch.bfloat16, dev, stream)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
     sg, su = gate.struct(), up.struct()
     if workspace is None:
         b = ctypes.c_size_t()
         _check(lib().patch_gemm_mlp_workspace_size(M, ctypes.byref(sg), ctypes.byref(su), ctypes.byref(b)),
                "patch_gemm_mlp_workspace_size")
-        workspace = torch.zeros(max(b.value, 16), dtype=torch.uint8, device=dev)  # must start zero-filled
+        workspace = _new(max(b.value, 16), torch.uint8, dev, stream, zero=True)  # must start zero-filled
     _check(lib().patch_gemm_mlp(_dev(X, "X"), M, ctypes.byref(sg), ctypes.byref(su), _dev(H, "H"),
                                 _dev(workspace, "workspace"), workspace.numel(), _dev(status, "status"),
                                 _stream(stream)), "patch_gemm_mlp")
@@ -533,7 +537,7 @@ def patch_mma_probe(sparse: bool, iters: int, status: torch.Tensor | None = None
     M = 128, N = 240 MMAs per SM on shared-memory operands); time it with CUDA
     events on the stream.  FLOPs per launch: SMs x iters x 4 x 2 x 128 x 240 x
     (32 if sparse else 16), dense-equivalent."""
-    status = new_status() if status is None else status
+    status = _new(1, torch.int32, "cuda", stream, zero=True) if status is None else status
     _check(lib().patch_mma_probe(1 if sparse else 0, iters, _dev(status, "status"), _stream(stream)),
            "patch_mma_probe")
 
@@ -542,7 +546,7 @@ def patch_check_weight(weight: PackedWeight, status: torch.Tensor | None = None,
     """Check a packed weight's descriptor table on the device (tile kinds, sparse
     ordinals, values offsets, sparse-tile count); a violation sets DEV_BOUNDS in
     the returned status word (read it with patch_read_status)."""
-    status = new_status(weight.desc.device) if status is None else status
+    status = _new(1, torch.int32, weight.desc.device, stream, zero=True, kept=True) if status is None else status
     st = weight.struct()
     _check(lib().patch_check_weight(ctypes.byref(st), _dev(status, "status"), _stream(stream)), "patch_check_weight")
     return status
@@ -595,8 +599,8 @@ def patch_exec_tiles64(bitmap: torch.Tensor, N: int, K: int, mask_tile: int,
     """64 x 64 execution tiles of a b x b mask bitmap (b <= 64): (exec u8 [N/64][K/64],
     n_sparse int64 [1]), on the device."""
     dev = bitmap.device
-    ex = torch.empty((N // TILE64, K // TILE64), dtype=torch.uint8, device=dev)
-    n_sparse = torch.empty(1, dtype=torch.int64, device=dev)
+    ex = _new((N // TILE64, K // TILE64), torch.uint8, dev, stream)
+    n_sparse = _new(1, torch.int64, dev, stream)
     _check(lib().patch_exec_tiles64(_dev(bitmap, "bitmap"), N, K, int(mask_tile), _dev(ex, "exec"),
                                     _dev(n_sparse, "n_sparse"), _stream(stream)), "patch_exec_tiles64")
     return ex, n_sparse
@@ -610,10 +614,10 @@ def patch_pack64(W: torch.Tensor, bitmap: torch.Tensor, pat_id: torch.Tensor, n_
         n_sparse = int(torch.count_nonzero(bitmap).item())
     vb, mb, db = patch_pack64_sizes(N, K, n_sparse)
     dev = W.device
-    status = new_status(dev) if status is None else status
-    values = torch.empty(vb, dtype=torch.uint8, device=dev)
-    meta = torch.empty(mb, dtype=torch.uint8, device=dev)
-    desc = torch.empty(db, dtype=torch.uint8, device=dev)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
+    values = _new(vb, torch.uint8, dev, stream)
+    meta = _new(mb, torch.uint8, dev, stream)
+    desc = _new(db, torch.uint8, dev, stream)
     _check(lib().patch_pack64(_dev(W, "W"), N, K, _dev(bitmap, "bitmap"), _dev(pat_id, "pat_id"), n_sparse,
                               _dev(values, "values"), _dev(meta, "meta") if mb else None, _dev(desc, "desc"),
                               _dev(status, "status"), _stream(stream)), "patch_pack64")
@@ -638,11 +642,11 @@ def patch_gemm64(X: torch.Tensor, weight: PackedWeight64, Y: torch.Tensor | None
         raise ValueError(f"X has K={K}, weight has K={weight.K}")
     dev = X.device
     if Y is None:
-        Y = torch.empty((M, weight.N), dtype=torch.bfloat16, device=dev)
-    status = new_status(dev) if status is None else status
+        Y = _new((M, weight.N), torch.bfloat16, dev, stream)
+    status = _new(1, torch.int32, dev, stream, zero=True) if status is None else status
     st = weight.struct()
     if workspace is None:
-        workspace = torch.zeros(max(patch_gemm64_workspace_size(M, weight), 16), dtype=torch.uint8, device=dev)
+        workspace = _new(max(patch_gemm64_workspace_size(M, weight), 16), torch.uint8, dev, stream, zero=True)
     _check(lib().patch_gemm64(_dev(X, "X"), M, ctypes.byref(st), _dev(Y, "Y"), _dev(workspace, "workspace"),
                               workspace.numel(), _dev(status, "status"), _stream(stream), wait_limit_us),
            "patch_gemm64")
@@ -652,7 +656,7 @@ def patch_gemm64(X: torch.Tensor, weight: PackedWeight64, Y: torch.Tensor | None
 def patch_mma_probe_m(m: int, sparse: bool, iters: int, status: torch.Tensor | None = None, stream=None) -> None:
     """patch_mma_probe for MMA shape M = 64 or 128: FLOPs per launch SMs x iters x 4 x 2 x m x 240 x
     (32 if sparse else 16), dense-equivalent."""
-    status = new_status() if status is None else status
+    status = _new(1, torch.int32, "cuda", stream, zero=True) if status is None else status
     _check(lib().patch_mma_probe_m(int(m), 1 if sparse else 0, iters, _dev(status, "status"), _stream(stream)),
            "patch_mma_probe_m")
 
