@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   };
   for (int s = 0; s < STAGES; ++s) fetch();
 
-  int done = 0;
+  int done = 0;  // chunks that have come and been used
+  bool lost = false;
   for (; cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
     const Tile& t = cur.t;
     // ---- the rows' queries as operands, each row divided by a power of two
@@ -233,8 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
     for (int c = cur.c; c < cur.c_end; ++c) {
       const int st = done % STAGES;
       const bool ok = tc::wait_bounded(bars + st, (done / STAGES) & 1, abort_flag, P.limit_ns, a.status, false);
+      lost = !__all_sync(0xFFFFFFFFu, ok);
+      if (lost) break;
       ++done;
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");  // this stage's scales
       __syncwarp();
       const uint8_t *ks_at = smem + warp * C::kRingBytes + st * 2 * kChunkBytes, *vs_at = ks_at + kChunkBytes;
@@ -452,6 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
       fetch();
     }
 
+    if (lost) break;  // nothing goes where copies may still land
+
     // ---- the tile's state over this warp's chunks: out, or kept as a piece
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -512,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
   }
   // after a timeout: let the copies in flight land before their memory is used again
   for (; done < issued; ++done)
-    tc::wait_bounded(bars + done % STAGES, (done / STAGES) & 1, abort_flag, P.limit_ns, a.status, true);
+    tc::wait_bounded(bars + done % STAGES, (done / STAGES) & 1, abort_flag, tc::kDrainNs, a.status, true);
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
   // ---- join the pieces: a run of one tile's pieces is the one that begins it (or comes in from the
   // CTA before) and the following warps' that entered it in the middle.  Every thread joins kEl

@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
   } else if (warp == 13) {
     // ================= loads: lane i < SL has the 16-token slice i of a block
     const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
-    int g = 0;
+    int g = 0, keys = 0, values = 0;  // keys, values: blocks whose copies have been issued
     bool ok = true;
     for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
       const Tile& t = cur.t;
@@ -677,9 +677,11 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         ok = g < 2 || wait(s_full + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.k_map, raw_k_at + (g & 1) * C::kRawBytes, raw_k + (g & 1));
+        keys = g + 1;
         ok = g < 2 || wait(raw_v_free + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.v_map, raw_v_at + (g & 1) * C::kRawBytes, raw_v + (g & 1));
+        values = g + 1;
         // the largest value scale and the smallest but 0 (none is negative: their order is that of their bits)
         const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sc.y)));
         const float least = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(sc.y > 0.0f ? sc.y : INFINITY)));
@@ -699,13 +701,12 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    if (!ok) {  // after a timeout: let the copies in flight land (one of each ring place at most is not awaited yet)
-      for (int i = 0; i < 2; ++i) {
-        const int last = g - 1 - i;
-        if (last < 0) break;
-        tc::wait_bounded(raw_k + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
-        tc::wait_bounded(raw_v + (last & 1), (last >> 1) & 1, abort_flag, P.limit_ns, a.status, true);
-      }
+    // Let the copies in flight land: one of each ring place at most is not awaited yet.  After a timeout, this
+    // warp's or another's, nobody else waits for them.
+    for (int i = 1; i <= 2; ++i) {
+      const int k = keys - i, v = values - i;
+      if (k >= 0) tc::wait_bounded(raw_k + (k & 1), (k >> 1) & 1, abort_flag, tc::kDrainNs, a.status, true);
+      if (v >= 0) tc::wait_bounded(raw_v + (v & 1), (v >> 1) & 1, abort_flag, tc::kDrainNs, a.status, true);
     }
   } else if (lane == 0) {
     // ================= the products
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
     }
     while (ok && pv < g) ok = product_pv();
     tc::tc_commit(drain);  // nothing in flight when the memory goes
-    tc::wait_bounded(drain, 0, abort_flag, P.limit_ns, a.status, true);
+    tc::wait_bounded(drain, 0, abort_flag, tc::kDrainNs, a.status, true);
   }
   tc::tc_fence_before();
   __syncthreads();

@@ -66,6 +66,10 @@ static __device__ __noinline__ bool wait_bounded_slow(uint64_t* bar, uint32_t pa
   }
 }
 
+// For the copies and products that are still under way when a wait has run out: they end by themselves within
+// microseconds, whatever limit the caller has set for the others.
+constexpr uint64_t kDrainNs = 2000000000ull;
+
 // Inline fast path: one try_wait, then the bounded slow loop if needed.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* abort_flag_smem, uint64_t limit_ns,
                                              int32_t* status, bool drain) {
