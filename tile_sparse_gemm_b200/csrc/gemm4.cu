@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
     fet.src = static_cast<const S*>(P.scales) + int64_t(min(16 * fet.tile + lane, P.N - 1)) * row_groups + (kb0 + fet.b0) * kGroups;
   };
   settle(false);
-  int issued = 0, done = 0;
+  int issued = 0, done = 0;  // done: blocks that have come and been used
+  bool lost = false;
   auto fetch = [&]() {  // the whole warp; one group of asynchronous copies a call, on every lane
     if (fet.chunk0 < groups) {
       const int st = issued % kStages;
@@ -388,11 +389,12 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
           for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[t][u][k] = 0.0f;
-        for (int blk = kw; blk < nb; blk += kKWarps) {
+        for (int blk = kw; !lost && blk < nb; blk += kKWarps) {
           const int st = done % kStages;
           const bool ok = tc::wait_bounded(bars + st, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, false);
+          lost = !__all_sync(0xFFFFFFFFu, ok);
+          if (lost) break;
           ++done;
-          if (!__all_sync(0xFFFFFFFFu, ok)) break;
           asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");  // this stage's scales
           __syncwarp();
           alignas(16) S sc[MT][2][kGroups];  // of rows n and n + 8
@@ -519,7 +521,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
   }
   // after a timeout: let the copies in flight land before the shared memory goes
   for (; done < issued; ++done)
-    tc::wait_bounded(bars + done % kStages, (done / kStages) & 1, abort_flag, 2000000000ull, P.status, true);
+    tc::wait_bounded(bars + done % kStages, (done / kStages) & 1, abort_flag, tc::kDrainNs, P.status, true);
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   if (kParts) cluster_wait();  // the others have read this CTA's sums
 }
