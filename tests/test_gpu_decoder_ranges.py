@@ -164,3 +164,14 @@ def test_attn_queries_at_the_ends_of_bf16(m, H, D):
             within(lse[rows], (x @ k) * scale, bound, f"lse {tops[b]}")
             v = (cache.v[b, 0, 0].double() * cache.v_scale[b, 0].double()).expand(m, H, D)
             within(out[rows], v, 2.0**-8 * v.abs() + 1e-30, f"out {tops[b]}")
+
+
+@pytest.mark.parametrize("N,K,group", [(5000, 4096, 32), (9000, 2080, 32), (700, 12800, 64), (96, 16384 + 32, 32), (3000, 24576, 128)])
+def test_gemm4_ctas_that_share_an_sm_or_not(N, K, group):
+    """X, its sums and the scales take shared memory by tokens, K and group: two CTAs an SM, one, or slices of K."""
+    g = gen(N)
+    w = tsg.Weight4(torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                    (0.5 + torch.rand(N, K // group, generator=g, device="cuda")).to(BF16), group)
+    for M in (1, 3, 4, 5, 8, 9, 13, 16):
+        x = torch.randn(M, K, generator=g, device="cuda").to(FP16)
+        within(tsg.patch_gemm4(x, w), *ref.gemm4(x, w.codes, w.scales, group), f"M={M}")

@@ -96,9 +96,10 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // are on their way), and their sums are added in shared memory in warp order
 // (deterministic).  A lane reads 4 bytes at a time, so that the four lanes of a
 // row hold a quarter each of every group of 32.  Up to 8 tokens: 8 warps, each
-// with both tiles (an operand of X serves two), two CTAs per SM.  Up to 16: 8
-// warps for either tile, one CTA per SM.  K beyond what X's place holds is taken
-// in slices, the sums of four row groups kept meanwhile by the threads that add them.
+// with both tiles (an operand of X serves two), two CTAs per SM where their shared
+// memory allows it and that is faster.  Up to 16: 8 warps for either tile, one CTA
+// per SM.  K beyond what X's place holds is taken in slices, the sums of four row
+// groups kept meanwhile by the threads that add them.
 //
 // Every CTA prepares all of X that it needs, which for few rows or many tokens takes
 // longer than the products.  So up to 8 CTAs may form a cluster: they share row groups,
@@ -108,7 +109,7 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // Measured: 128000 x 4096, 1 token, group 32: 69 us (codes and scales, 295 MB, at 4.3
 // TB/s; fetching alone takes 46 us, the rest is what the integer and tensor instructions
 // of a block take beyond that); 14336 x 4096, 16 tokens: 23.5 us, of which 5 prepare X in
-// every CTA and 11 are the products; 4096 x 4096, 1 token: 6.2 us, mostly latency.
+// every CTA and 11 are the products; 4096 x 4096, 1 token: 5.0 us, mostly latency.
 namespace g4 {
 
 constexpr int kBlockK = 256, kBoxBytes = 16 * 128;
@@ -126,6 +127,7 @@ struct Params {
 constexpr int kKWarps = 8;  // warps that share a row tile's blocks of k
 constexpr int kGroupRows = 32;
 constexpr int kMaxParts = 8;  // the portable size of a cluster
+constexpr int kSmemOfSm = 228 * 1024, kSmemReserved = 1024;  // shared memory; what each CTA takes beside its own
 constexpr int kKept = 4;  // row groups whose sums are kept over slices, in registers
 
 template <int NT>
@@ -134,7 +136,6 @@ struct Cfg {
   static constexpr int MT = 2 / kRowWarps;                // row tiles of a warp
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = MT * kBoxBytes;
-  static constexpr int kXBytes = NT == 1 ? 32768 : 131072;  // 2048 or 4096 k of the most tokens
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
 
@@ -532,33 +533,40 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   using C = Cfg<NT>;
   P.tiles = (P.N + 15) / 16;
   P.blocks = (P.K + kBlockK - 1) / kBlockK;
-  // a slice: whole rounds of the warps, as many as fit
-  const int fit = C::kXBytes / P.M / (kBlockK * 2) / kKWarps * kKWarps;
-  // Parts of K, by an estimate of a CTA's time in ns: X of a block and token 20 (again for every chunk of row groups
-  // where K is taken in slices), a row group's products of a block 165 (both tiles' warps) or 300 (two CTAs an SM),
-  // its sums 300, 1500 with each slice, or 2200 through the cluster.  Measured with one part and with the chosen:
+  // Parts of K, and one or two CTAs an SM (which have to fit: X, its sums and the scales grow with tokens, K and finer
+  // groups), by an estimate of a CTA's time in ns: X of a block and token 20 (again for every chunk of row groups where
+  // K is taken in slices), a row group's products of a block 165 (both tiles' warps), 180 (8 warps alone on their SM)
+  // or 300 (two CTAs an SM), its sums 300, 1500 with each slice, or 2200 through the cluster.
+  // Measured, two CTAs an SM and one: 128000 x 4096, group 128, 1 token 50 us, 58; 6 tokens 84, 65; 9000 x 11008,
+  // group 32, 4 tokens 38, 25; where two do not fit, 8 tokens and group 32, 128000 x 4096 142 as two waves, 81.
+  // Measured with one part and with the chosen:
   // 577 x 11072, 14 tokens 31 us, 12 (4 parts); 4096 x 14336, 8 tokens 39, 20 (8), 16 tokens 37, 25 (4); 256 x
   // 14336, 1 token 12.3, 6.4 (8); 4096 x 4096, 1 token 7.1, 6.4 (2).  One part stays where the others lose: 4096 x
   // 4096, 16 tokens 11.9, 12.3 with two; 14336 x 4096, 16 tokens 23, 28; 128000 x 4096, 1 token 66, 107.
   float best = 0.0f;
   int grid = 0;
-  for (int parts = 1; parts <= kMaxParts && parts <= P.blocks; parts *= 2) {
-    const int local = (P.blocks + parts - 1) / parts;
-    // clusters that run at once: they lie in one of the GPU's parts of 16 to 20 SMs each (33 of 4, 15 of 8 on 148 SMs)
-    const int most = C::kCtas * num_sms * (parts <= 2 ? 16 : parts == 4 ? 14 : 13) / 16 / parts;
-    const bool slices = local > fit;
-    if (parts > 1 && (slices || most < 1)) continue;
-    const int shares = P.tiles < most ? P.tiles : most, groups = ((P.tiles + shares - 1) / shares + 1) / 2;
-    const float times = slices ? float((groups + kKept - 1) / kKept) : 1.0f;
-    const float sums = parts > 1 ? 2200.0f : slices ? 300.0f + 1500.0f * float((local + fit - 1) / fit) : 300.0f;
-    const float ns = 20.0f * float(P.M) * float(local) * times +
-                     float(groups) * ((NT == 1 ? 300.0f : 165.0f) * float(local) + sums);
-    if (parts > 1 && ns >= best) continue;
-    best = ns;
-    grid = shares * parts;
-    P.parts = parts;
-    P.slice_blocks = slices ? fit : local;
-    P.chunk = slices && groups > kKept ? kKept : groups;
+  for (int ctas = C::kCtas; ctas >= 1; --ctas) {
+    auto fits = [&](int x_blocks) { return layout<NT, GS>(P.M, x_blocks).bytes <= kSmemOfSm / ctas - kSmemReserved; };
+    int slice = (P.blocks - 1) / kKWarps * kKWarps;  // whole rounds of the warps, as many as fit
+    while (slice > 0 && !fits(slice)) slice -= kKWarps;
+    for (int parts = 1; parts <= kMaxParts && parts <= P.blocks; parts *= 2) {
+      const int local = (P.blocks + parts - 1) / parts;
+      // clusters that run at once: they lie in one of the GPU's parts of 16 to 20 SMs each (33 of 4, 15 of 8 on 148 SMs)
+      const int most = ctas * num_sms * (parts <= 2 ? 16 : parts == 4 ? 14 : 13) / 16 / parts;
+      const bool slices = !fits(local);
+      if (most < 1 || (slices && (parts > 1 || slice == 0))) continue;
+      const int shares = P.tiles < most ? P.tiles : most, groups = ((P.tiles + shares - 1) / shares + 1) / 2;
+      const float times = slices ? float((groups + kKept - 1) / kKept) : 1.0f;
+      const float sums = parts > 1 ? 2200.0f : slices ? 300.0f + 1500.0f * float((local + slice - 1) / slice) : 300.0f;
+      const float ns = 20.0f * float(P.M) * float(local) * times +
+                       float(groups) * ((ctas == 2 ? 300.0f : NT == 1 ? 180.0f : 165.0f) * float(local) + sums);
+      if (grid && ns >= best) continue;
+      best = ns;
+      grid = shares * parts;
+      P.parts = parts;
+      P.slice_blocks = slices ? slice : local;
+      P.chunk = slices && groups > kKept ? kKept : groups;
+    }
   }
   const Layout L = layout<NT, GS>(P.M, P.slice_blocks);
   const bool vec = P.K % kBlockK == 0;
