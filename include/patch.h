@@ -898,8 +898,9 @@ PATCH_API patch_status_t patch_quantize4(const void *W, int dtype, const patch_w
  * vocabulary head, small projections).  X [M][K] and Y [M][N] bf16 or fp16
  * (16-byte aligned X), fp32 sums, one rounding.  No workspace; deterministic.
  * X enters the tensor cores as fp16, every 128 elements of a token divided by a
- * power of two first (elements below 2^-28 of the largest lose bits, less than
- * 2^-39 of it); a token with an infinity or NaN in it gives NaN.  A bounded wait
+ * power of two first (elements below 2^-24 of the largest lose bits, at most
+ * 2^-35 of it); the codes' products and their offset's, 8 |x| scale, are summed in
+ * fp32; a token with an infinity or NaN in it gives NaN.  A bounded wait
  * (2 s) that runs out sets PATCH_DEV_TIMEOUT.  dev_status may be NULL.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, M outside 0 .. 16, group, dtypes),
  * PATCH_ERR_SHAPE (N < 1, K not a positive multiple of group, either > 2^30),

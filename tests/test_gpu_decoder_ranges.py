@@ -175,3 +175,42 @@ def test_gemm4_ctas_that_share_an_sm_or_not(N, K, group):
     for M in (1, 3, 4, 5, 8, 9, 13, 16):
         x = torch.randn(M, K, generator=g, device="cuda").to(FP16)
         within(tsg.patch_gemm4(x, w), *ref.gemm4(x, w.codes, w.scales, group), f"M={M}")
+
+
+FAR_BELOW = 2.0**-35  # of the largest of a token's 128 elements: what one of them may be off by
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("place", range(8))
+def test_gemm4_elements_far_below_the_largest(dtype, place):
+    """Elements 2^-32 to 2^-34 of the largest of their 128, which has a group of its own with weights of zero: each place of
+    the operand order (8 elements) in turn holds them.  Beside FAR_BELOW of the largest, fp32 sums of up to 15 |x| s and
+    8 |x| s, an addition a k, each off by 2^-24."""
+    N, K, group, M = 64, 512, 32, 5
+    g = gen(71)
+    c = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda")
+    c.view(N, -1, 64)[:, :, :16] = 0x88  # the first group of each 128 k
+    w = tsg.Weight4(c, (0.5 + torch.rand(N, K // group, generator=g, device="cuda")).to(BF16), group)
+    k = torch.arange(K, device="cuda")
+    e = torch.randint(22, 25, (M, K), generator=g, device="cuda").double()
+    x = torch.where((k % 8 == place) & (k % 128 >= 32), (1 + torch.rand(M, K, generator=g, device="cuda").double()) * 2.0**-e, 0.0)
+    x[:, 5::128] = 1024.0
+    x = x.to(dtype)
+    y, bound = ref.gemm4(x, c, w.scales, group)
+    wd = (torch.stack((c & 15, c >> 4), -1).flatten(1).double() - 8.0).abs() * w.scales.double().repeat_interleave(group, 1)
+    s = w.scales.double().repeat_interleave(group, 1) * (k % 128 >= 32)
+    few = (k % 8 == place).double()
+    bound = bound + 2.0**-24 * 23 * (group + 2) * x.double().abs() @ s.T + FAR_BELOW * 1024.0 * few @ wd.T
+    within(tsg.patch_gemm4(x, w), y, bound)
+
+
+def test_gemm4_a_token_with_an_infinity_is_nan():
+    g = gen(72)
+    w = tsg.patch_quantize4(torch.randn(40, 256, generator=g, device="cuda"), 64)
+    for dtype in (BF16, FP16):
+        x = torch.randn(12, 256, generator=g, device="cuda").to(dtype)
+        clean = tsg.patch_gemm4(x, w)
+        x[3, 70], x[9, 255] = math.inf, -math.inf
+        y = tsg.patch_gemm4(x, w)
+        rest = [m for m in range(12) if m not in (3, 9)]
+        assert bool(y[[3, 9]].isnan().all()) and torch.equal(y[rest], clean[rest])

@@ -87,8 +87,9 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 //
 // X is put in shared memory as fp16 in operand order (per 8 k: the pairs (0,4)
 // (1,5) (2,6) (3,7)), every 128 elements of a token divided by a power of two
-// that brings their largest into [2^14, 2^15): bf16 and fp16 values down to 2^-28
-// of it stay exact, smaller ones are off by less than 2^-39 of it.
+// that brings their largest into [2^14, 2^15): bf16 and fp16 values down to 2^-24 of
+// it stay exact, smaller ones are off by at most 2^-35 of it (2^-39 where the partner
+// is not divided by 16).
 //
 // A CTA has an equal share of the row tiles of 16 and takes two at a time (a row
 // group); its warps take the group's blocks of 256 k in turn, 128 bytes of each
