@@ -214,3 +214,36 @@ def test_gemm4_a_token_with_an_infinity_is_nan():
         y = tsg.patch_gemm4(x, w)
         rest = [m for m in range(12) if m not in (3, 9)]
         assert bool(y[[3, 9]].isnan().all()) and torch.equal(y[rest], clean[rest])
+
+
+def state(c):
+    return [t.view(torch.uint8).clone() for t in (c.k, c.v, c.k_scale, c.v_scale)]
+
+
+@pytest.mark.parametrize("many", [False, True])  # small CTAs and page-wide ones
+def test_append_beyond_the_table_writes_neither_keys_nor_values(many):
+    """A page with a token whose position has no angles is left as it is, keys, values and both scales; others are not."""
+    page, d, hk = 16, 64, 2
+    g = gen(81)
+    table = tsg.patch_rope_table(40, d)
+    new = 20 if many else 1
+    past = [39, 40, 47, 30] if not many else [24, 32, 30]
+    B = len(past)
+    bt = i32([[4 * b + j for j in range(4)] for b in range(B)])
+    cache = random_cache(4 * B, hk, page, d, g)
+    k, v = ((4 * torch.randn(B * new, hk, d, generator=g, device="cuda")).to(BF16) for _ in range(2))
+    for b, p in enumerate(past):
+        was = state(cache)
+        st = tsg.new_status()
+        rows = slice(b * new, (b + 1) * new)
+        tsg.patch_kv8_append(k[rows], v[rows], cache, bt[b : b + 1], i32([p]), i32([0, new]), table, status=st)
+        bad = p + new > 40
+        assert tsg.patch_read_status(st)[1] == (tsg.DEV_BOUNDS if bad else 0)
+        now = state(cache)
+        for q in range(4 * B):
+            first, last = max(p, (q - 4 * b) * page), min(p + new, (q - 4 * b + 1) * page)  # of this call's tokens in it
+            written = q // 4 == b and first < last <= 40
+            for i, (x, y) in enumerate(zip(was, now)):
+                same = torch.equal(x[q], y[q])
+                assert same or written, (p, q, i)
+                assert not (same and written and i < 2), (p, q, i)  # a scale may stay

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv8_append_kernel(c
     raw0 = *reinterpret_cast<const uint4*>(src + u.d0);
     raw1 = *reinterpret_cast<const uint4*>(src + u.d1);
   }
-  if (t.phys < 0 || t.phys >= P.n_pages || (turn && t.begin + t.count > P.n_pos)) {
+  if (t.phys < 0 || t.phys >= P.n_pages || (P.rot_units > 0 && t.begin + t.count > P.n_pos)) {
     if (threadIdx.x == 0) set_status(P.status, PATCH_DEV_BOUNDS);
     return;
   }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(64) kv8_append_few_kernel(const __grid_constan
   const int which = blockIdx.z, h = blockIdx.y;
   const bool turn = which == 0 && P.rot_units > 0;
   const T* src = static_cast<const T*>(P.x[which]) + t.row * P.ts[which] + h * P.hs[which];
-  if (t.phys < 0 || t.phys >= P.n_pages || (turn && t.begin + t.count > P.n_pos)) {
+  if (t.phys < 0 || t.phys >= P.n_pages || (P.rot_units > 0 && t.begin + t.count > P.n_pos)) {
     if (threadIdx.x == 0) set_status(P.status, PATCH_DEV_BOUNDS);
     return;
   }
