@@ -247,3 +247,33 @@ def test_append_beyond_the_table_writes_neither_keys_nor_values(many):
                 same = torch.equal(x[q], y[q])
                 assert same or written, (p, q, i)
                 assert not (same and written and i < 2), (p, q, i)  # a scale may stay
+
+
+@pytest.mark.parametrize("page,B", [(16, 1), (64, 40)])
+@pytest.mark.parametrize("past,new", [(-1, 1), (-5, 3), (-20, 20), (-3, 40), (-(2**31), 1)])
+def test_append_to_a_negative_length_is_refused(page, B, past, new):
+    """The only wrong sequence of a call, alone or last of many: reported, nothing of it stored, the others as ever."""
+    d, hk = 64, 2
+    g = gen(82)
+    lens, news = [3] * (B - 1) + [past], [new] * B
+    bt = torch.arange(4 * B, dtype=torch.int32, device="cuda").view(B, 4)
+    cache = random_cache(4 * B, hk, page, d, g)
+    was, other = state(cache), copy_of(cache)
+    x = torch.randn(B * new, hk, d, generator=g, device="cuda").to(BF16)
+    cu = i32([new * b for b in range(B + 1)])
+    st = tsg.new_status()
+    tsg.patch_kv8_append(x, x, cache, bt, i32(lens), cu, status=st)
+    assert tsg.patch_read_status(st)[1] == tsg.DEV_BOUNDS
+    for a, b in zip(was, state(cache)):
+        assert torch.equal(a[4 * (B - 1) :], b[4 * (B - 1) :])
+    if B > 1:
+        tsg.patch_kv8_append(x[:-new], x[:-new], other, bt[:-1].contiguous(), i32(lens[:-1]), cu[:-1])
+        for a, b in zip(state(other), state(cache)):
+            assert torch.equal(a[: 4 * (B - 1)], b[: 4 * (B - 1)])
+    if new == 1:
+        st.zero_()
+        tsg.patch_kv8_append(x, x, cache, bt, i32(lens), status=st)
+        assert tsg.patch_read_status(st)[1] == tsg.DEV_BOUNDS
+    st.zero_()  # no new tokens: nothing to refuse
+    tsg.patch_kv8_append(x[:0], x[:0], cache, bt, i32(lens), i32([0] * (B + 1)), status=st)
+    assert tsg.patch_read_status(st) == (0, 0)

@@ -68,14 +68,15 @@ __device__ __forceinline__ Touched touched(const AppendParams& P, int64_t item) 
     row0 = b;
   }
   const int past = P.past_lens[b];
+  const bool bad = past < 0;  // none of its tokens is stored; its first item says so
   const int64_t page_no = max(past, 0) / P.page + j;
   const int64_t begin = max(int64_t(past), page_no * P.page), end = min(past + n, (page_no + 1) * P.page);
-  if (begin >= end) return t;
+  if (begin >= end && (!bad || j > 0 || n <= 0)) return t;
   t.begin = begin;
-  t.count = int(end - begin);
+  t.count = max(int(end - begin), 1);
   t.off = int(begin - page_no * P.page);
-  t.row = row0 + begin - past;
-  t.phys = past >= 0 && page_no < P.max_pages ? P.block_table[b * P.max_pages + page_no] : -1;
+  t.row = bad ? row0 : row0 + begin - past;
+  t.phys = !bad && page_no < P.max_pages ? P.block_table[b * P.max_pages + page_no] : -1;
   return t;
 }
 
