@@ -853,7 +853,8 @@ PATCH_API patch_status_t patch_kv8_append(const patch_heads *k, const patch_head
  *              its counters zero again, so one serves any number of calls of any
  *              sizes on one stream.  Calls that may run at the same time need one each.
  * A page id outside the pool, or kv_lens[b] outside 0 .. max_pages * page, sets
- * PATCH_DEV_BOUNDS (the tokens there read as zeros; the length is clamped).
+ * PATCH_DEV_BOUNDS (the tokens there read as zeros; the length is clamped).  The id of
+ * a page wholly before the window of all of a sequence's queries may be anything.
  * Bounded waits as patch_gemm (wait_limit_us, 0 = 2 s); after one that ran out
  * (PATCH_DEV_TIMEOUT) zero the workspace again.  dev_status may be NULL.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts, dtype, n_tokens != batch without cu_q, scale not

@@ -34,6 +34,7 @@ def attention_of_own(q, c, bt, kv, m, scale, causal, window):
         ids[: lo // page] = 0
         k, v = ((x.view(torch.uint8)[ids].view(F8).double() * s[ids].double()[..., None, None]).transpose(0, 1).reshape(hk, -1, D)[:, :n]
                 for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+        k[:, :lo] = v[:, :lo] = 0.0
         rows = slice(b * m, (b + 1) * m)
         s = torch.einsum("mhgd,hnd->mhgn", q[rows].double().view(m, hk, g, D), k) * scale
         s = s.masked_fill(hidden[:, None, None, :].expand_as(s), -math.inf)
@@ -277,3 +278,26 @@ def test_append_to_a_negative_length_is_refused(page, B, past, new):
     st.zero_()  # no new tokens: nothing to refuse
     tsg.patch_kv8_append(x[:0], x[:0], cache, bt, i32(lens), i32([0] * (B + 1)), status=st)
     assert tsg.patch_read_status(st) == (0, 0)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("window", [1, 37, 150])
+def test_attn_pages_before_the_window(window, tile, D, page):
+    """Pages that no query sees any more may have been given back: their ids are anything, without a report, or theirs
+    are pages of others, full of NaN under any scale."""
+    m, kv = tile[0], (700, 333)
+    for spoilt in (-1, 2**31 - 1, None):
+        def edit(q, c, bt):
+            for b, n in enumerate(kv):
+                gone = max(0, n - m - window + 1) // page
+                if spoilt is not None:
+                    bt[b, :gone] = spoilt
+                else:
+                    ids = bt[b, :gone].long()
+                    for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+                        x.view(torch.uint8)[ids] = 0x7F
+                        s[ids] = math.inf
+            return q
+        attend(tile, D, BF16, edit, page=page, kv=kv, window=window)

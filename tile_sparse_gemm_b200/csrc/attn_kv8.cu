@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
         const int tok = t0 + (lane << P.box_shift), in_page = tok & (a.page - 1);
         const int phys = a.block_table[fet.t.b * a.max_pages + (tok >> P.page_shift)];
         const bool ok = phys >= 0 && phys < a.n_pages;
-        if (!ok) set_status(a.status, PATCH_DEV_BOUNDS);
+        if (!ok && tok + box > fet.t.lo) set_status(a.status, PATCH_DEV_BOUNDS);  // else before the window
         const int blk = ok ? phys * a.kv_heads + fet.t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
         const uint32_t dst = ring + st * 2 * kChunkBytes + lane * (D << P.box_shift);
         tma_load_3d(dst, &P.k_map, bar, 0, in_page, blk);

@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         const int n_box = max(min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift), 0);
         const uint32_t bytes = uint32_t(n_box * D) << P.box_shift;
         const bool in = in_pool(phys), wanted = lane < SL && tok < t.hi;
-        if (wanted && !in) set_status(a.status, PATCH_DEV_BOUNDS);
+        if (wanted && !in && tok + 16 > t.lo) set_status(a.status, PATCH_DEV_BOUNDS);  // else before the window
         const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
         const bool leads = wanted && (16 * lane & (box - 1)) == 0;
         auto issue = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
