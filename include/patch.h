@@ -885,7 +885,7 @@ typedef struct {
 
 /*
  * patch_quantize4: W (bf16, fp16 or fp32 [N][K]) to 4 bits, nearest code under
- * a group's scale amax / 7 (rounded to scale_dtype before the codes are taken):
+ * a group's scale amax / 7 (rounded to scale_dtype before the codes are taken, at most its largest number):
  * code = 8 + clamp(round(w / scale), -8, 7), ties to even; a group of zeros has scale 0 and codes 8.
  * amax runs over the finite weights; infinities saturate and NaN becomes code 8.
  * N, K, group and scale_dtype are taken from *out, whose codes and scales it

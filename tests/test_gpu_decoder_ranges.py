@@ -301,3 +301,23 @@ def test_attn_pages_before_the_window(window, tile, D, page):
                         s[ids] = math.inf
             return q
         attend(tile, D, BF16, edit, page=page, kv=kv, window=window)
+
+
+def test_quantize4_weights_beyond_a_fp16_scale():
+    """amax / 7 above 65504: the scale is fp16's largest number, the weights saturate, zeros stay zeros."""
+    w = torch.zeros(3, 128, device="cuda")
+    w[0, :4] = torch.tensor([1e6, -1e6, 3e5, -4e4])
+    w[1, 5:7] = torch.tensor([3.4e38, -3.4e38])
+    w[2, 0] = 458528.0  # 7 times the largest scale
+    q = tsg.patch_quantize4(w, 64, FP16)
+    c = torch.stack((q.codes & 15, q.codes >> 4), -1).flatten(1).int() - 8
+    assert bool((q.scales[:, 0] == 65504.0).all()) and bool((q.scales[:, 1] == 0.0).all())
+    want = torch.zeros_like(c)
+    want[0, :4] = torch.tensor([7, -8, 5, -1], dtype=torch.int32)
+    want[1, 5:7] = torch.tensor([7, -8], dtype=torch.int32)
+    want[2, 0] = 7
+    assert torch.equal(c, want)
+    x = torch.zeros(1, 128, dtype=BF16, device="cuda")
+    x[0, 10] = 1.0
+    assert not tsg.patch_gemm4(x, q).any()
+    assert torch.equal(tsg.patch_quantize4(w, 64, BF16).scales[:, 0].float(), (w[:, :64].abs().amax(1) / 7).to(BF16).float())

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256) quantize4_kernel(const T* __restrict__ W,
       s = to_f32(r);
       if (lead) static_cast<__nv_bfloat16*>(scales)[gi] = r;
     } else {
-      const __half r = __float2half_rn(s0);
+      const __half r = __float2half_rn(fminf(s0, 65504.0f));  // fp16's largest: an infinite scale has no codes
       s = to_f32(r);
       if (lead) static_cast<__half*>(scales)[gi] = r;
     }
