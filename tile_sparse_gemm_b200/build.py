@@ -1,5 +1,6 @@
-"""Build libpatch.so in-tree with nvcc for sm_100a (B200), and the CPython
-extension of the decode step's calls beside it.
+"""Build libpatch.so in-tree with nvcc for sm_100a (B200), and beside it, where
+this torch has CUDA and its headers, the CPython extension of the decode step's
+calls (without it they take their way through Python).
 
     python -m tile_sparse_gemm_b200.build          # compile if sources changed
     python -m tile_sparse_gemm_b200.build --force  # always recompile
@@ -44,6 +45,19 @@ def _stale(lib: Path) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def no_binding() -> str | None:
+    """Why the extension cannot be built here (the library needs nvcc alone), or None."""
+    try:
+        import torch
+    except ImportError as e:
+        return str(e)
+    home = Path(torch.__file__).resolve().parent
+    needed = [home / "lib" / "libtorch_cuda.so", home / "include" / "c10" / "cuda" / "CUDAStream.h",
+              Path(sysconfig.get_paths()["include"]) / "Python.h"]
+    missing = [str(p) for p in needed if not p.exists()] + ([] if shutil.which("g++") else ["g++"])
+    return f"missing: {', '.join(missing)}" if missing else None
+
+
 def build_binding(force: bool = False) -> Path:
     """_decoder_binding.so: against this interpreter's and this torch's headers."""
     import torch
@@ -67,10 +81,18 @@ def build_binding(force: bool = False) -> Path:
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> Path:
     lib = LIB_DEBUG if debug else LIB
+    if force or _stale(lib):
+        _build_library(lib, verbose, debug)
     if not debug:
-        build_binding(force)
-    if not force and not _stale(lib):
-        return lib
+        why = no_binding()
+        if why:
+            print(f"{BINDING.name} is left out: {why}", file=sys.stderr)
+        else:
+            build_binding(force)
+    return lib
+
+
+def _build_library(lib: Path, verbose: bool, debug: bool) -> None:
     build_dir = PKG / ("_build_debug" if debug else "_build")
     build_dir.mkdir(exist_ok=True)
     extra = ["-DPATCH_DEBUG"] if debug else []
@@ -90,7 +112,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> Pa
     subprocess.run([_nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", str(tmp), *objs,
                     "-lcudart"], check=True)
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":

@@ -7,18 +7,22 @@ kernels.  The calls run on the tensors' own device and on `stream` (default:
 that device's current stream), launch only libpatch kernels, allocate only the
 outputs and workspace they are not given (on that stream), never synchronise and
 can be captured in a CUDA graph.  Who passes a `stream` orders it after the inputs'
-writers and before the results' readers, and keeps the inputs until it is done.  A device status word is optional: `status=new_status()` collects what
-the kernels report (patch_read_status).
+writers and before the results' readers, and keeps the inputs until it is done.  A
+device status word is optional: `status=new_status()` collects what the kernels report
+(patch_read_status).  Nothing is recorded for autograd; patch_rope(backward=True) is
+the gradient of patch_rope.
 
 The calls of a decode step take less time on the device than their checks take
 in Python, so the ordinary ones (as documented, current device and stream) go
 through a compiled extension, csrc/decoder_binding.cpp.  It leaves every other
-call, the wrong ones among them, to the same checks here, which name the fault.
+call, the wrong ones among them, to the same checks here, which name the fault;
+without it (another torch than it was built for) all calls come here.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -78,20 +82,31 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _binding = None
 
 
+class _ThroughPython:
+    """In the place of the extension: leaves every call to the way through Python."""
+
+    @staticmethod
+    def rope(*_):
+        return None
+
+    append = attn = gemm4 = rope
+
+
 def _fast():
-    """The compiled extension, bound to the library's entry points."""
+    """The compiled extension, bound to the library's entry points; where it is missing, the same calls are made from here."""
     global _binding
     if _binding is None:
         library = lib()
         try:
             from . import _decoder_binding
         except ImportError as e:
-            raise ImportError("the compiled binding is missing or was built for another torch: build it with "
-                              "`python -m tile_sparse_gemm_b200.build`") from e
-
-        _decoder_binding.bind(*(ctypes.cast(getattr(library, "patch_" + f), ctypes.c_void_p).value
-                                for f in ("rope", "kv8_append", "attn_kv8", "gemm4")))
-        _binding = _decoder_binding
+            warnings.warn(f"the compiled binding is missing or was built for another torch ({e}): calls take their way through "
+                          "Python, some 10 us more each; build it with `python -m tile_sparse_gemm_b200.build`", stacklevel=3)
+            _binding = _ThroughPython
+        else:
+            _decoder_binding.bind(*(ctypes.cast(getattr(library, "patch_" + f), ctypes.c_void_p).value
+                                    for f in ("rope", "kv8_append", "attn_kv8", "gemm4")))
+            _binding = _decoder_binding
     return _binding
 
 
