@@ -5,12 +5,13 @@
 //
 // Each function does the ordinary call: every argument as documented, on the
 // current device and stream.  Anything else (another device, a wrong type or
-// shape) makes it return None without having done anything, and the caller
+// shape, a torch dispatch mode that watches allocations) makes it return None without having done anything, and the caller
 // (decoder.py) takes its own way through the same checks, which name the fault.
 // A status code other than PATCH_OK comes back as an int.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -62,7 +63,10 @@ struct Args {
     ok = false;
     return nullptr;
   }
-  bool current() const { return ok && device == c10::cuda::current_device(); }
+  // ... and a torch dispatch mode, which would not see the outputs' allocation
+  bool current() const {
+    return ok && device == c10::cuda::current_device() && !c10::impl::TorchDispatchModeTLS::any_modes_set();
+  }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(device).stream(); }
   int32_t* status(PyObject* o) {
     if (o == Py_None) return nullptr;
