@@ -321,3 +321,22 @@ def test_quantize4_weights_beyond_a_fp16_scale():
     x[0, 10] = 1.0
     assert not tsg.patch_gemm4(x, q).any()
     assert torch.equal(tsg.patch_quantize4(w, 64, BF16).scales[:, 0].float(), (w[:, :64].abs().amax(1) / 7).to(BF16).float())
+
+
+@pytest.mark.parametrize("kv,m,H,hk,D,dtype", [([1500], 1, 32, 32, 128, BF16), ([100 + 233 * i for i in range(30)], 1, 32, 8, 128, BF16),
+                                               ([90000], 1, 32, 8, 128, FP16), ([3000, 50, 4321], 9, 14, 2, 64, BF16),
+                                               ([1000, 5000], 300, 32, 8, 128, FP16)])
+def test_attn_repeats_itself(kv, m, H, hk, D, dtype):
+    """Tiles are cut between warps and CTAs, whose parts are joined in their order, whoever comes last: the same bits."""
+    g = gen(91)
+    bt, n_pages = pages_of(kv, 32, g)
+    c = random_cache(n_pages, hk, 32, D, g)
+    q = torch.randn(m * len(kv), H, D, generator=g, device="cuda").to(dtype)
+    args = (q, c, bt, i32(kv), i32([m * i for i in range(len(kv) + 1)]))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    out, lse = tsg.patch_attn_kv8(*args, want_lse=True)
+    for i in range(12):
+        if i % 2:
+            flush.fill_(i)
+        again, l = tsg.patch_attn_kv8(*args, want_lse=True)
+        assert torch.equal(out, again) and torch.equal(lse, l)
