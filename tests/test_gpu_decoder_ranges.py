@@ -340,3 +340,25 @@ def test_attn_repeats_itself(kv, m, H, hk, D, dtype):
             flush.fill_(i)
         again, l = tsg.patch_attn_kv8(*args, want_lse=True)
         assert torch.equal(out, again) and torch.equal(lse, l)
+
+
+def test_gemm4_k_whose_x_passes_32_bits():
+    """16 tokens of 2^26 and a few k: X has 2^31 bytes and more, taken in slices; a token at a time in 64 bits."""
+    N, K, group, M = 3, 2**26 + 128, 128, 16
+    g = gen(101)
+    w = tsg.Weight4(torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+                    (0.5 + torch.rand(N, K // group, generator=g, device="cuda")).to(BF16), group)
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.float16)
+    st = tsg.new_status()
+    y = tsg.patch_gemm4(x, w, status=st)
+    assert tsg.patch_read_status(st) == (0, 0)
+    for m in (0, 7, 15):
+        want, mag = torch.zeros(N, dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+        for k0 in range(0, K, 1 << 23):
+            k1 = min(K, k0 + (1 << 23))
+            c, s = w.codes[:, k0 // 2 : k1 // 2], w.scales[:, k0 // group : k1 // group]
+            a, _ = ref.gemm4(x[m : m + 1, k0:k1], c, s, group)
+            want += a[0]
+            mag += (8 * s.double().repeat_interleave(group, 1) * x[m, k0:k1].double().abs()).sum(1)
+        # 8 warps' sums of K / 8 each: a block of 256 k adds its part to a running sum, off by 2^-24 of what that holds
+        within(y[m], want, ref.HALF[FP16] * want.abs() + 2.0**-24 * (K / 2048) ** 0.5 * mag, f"token {m}")

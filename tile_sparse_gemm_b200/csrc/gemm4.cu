@@ -129,6 +129,7 @@ constexpr int kKWarps = 8;  // warps that share a row tile's blocks of k
 constexpr int kGroupRows = 32;
 constexpr int kMaxParts = 8;  // the portable size of a cluster
 constexpr int kSmemOfSm = 228 * 1024, kSmemReserved = 1024;  // shared memory; what each CTA takes beside its own
+constexpr int kMostBlocks = kSmemOfSm / (kBlockK * 2);  // of X in an SM, of one token
 constexpr int kKept = 4;  // row groups whose sums are kept over slices, in registers
 
 template <int NT>
@@ -547,8 +548,10 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   float best = 0.0f;
   int grid = 0;
   for (int ctas = C::kCtas; ctas >= 1; --ctas) {
-    auto fits = [&](int x_blocks) { return layout<NT, GS>(P.M, x_blocks).bytes <= kSmemOfSm / ctas - kSmemReserved; };
-    int slice = (P.blocks - 1) / kKWarps * kKWarps;  // whole rounds of the warps, as many as fit
+    auto fits = [&](int x_blocks) {
+      return x_blocks <= kMostBlocks && layout<NT, GS>(P.M, x_blocks).bytes <= kSmemOfSm / ctas - kSmemReserved;
+    };
+    int slice = (P.blocks > kMostBlocks ? kMostBlocks : P.blocks - 1) / kKWarps * kKWarps;  // whole rounds of the warps, as many as fit
     while (slice > 0 && !fits(slice)) slice -= kKWarps;
     for (int parts = 1; parts <= kMaxParts && parts <= P.blocks; parts *= 2) {
       const int local = (P.blocks + parts - 1) / parts;
