@@ -649,10 +649,10 @@ static cudaError_t launch(const Params& P, int num_sms, cudaStream_t stream) {
 static size_t attn_counter_bytes(int num_sms) { return (size_t(num_sms) * 4 + 255) / 256 * 256; }
 
 // Tiles of 128 rows (attn_kv8_rows.cu) where a sequence and head have 64 query rows or more on average.
-// Few-row kernel against the other, 8 sequences of 2000 tokens, 32 heads over 8 of 128: 32 rows 27 us, 34;
-// 48 rows 34, 34; 64 rows 39, 35; 128 rows 62, 36.  One of 16000: 64 rows 40, 53; 128 rows 61, 52.  64 of 500,
-// 16 over 4 of 64: 48 rows 27, 34; 64 rows 31, 34; 96 rows 40, 34.  One prompt among 63 single tokens over 2048
-// tokens each: 256 queries (20 rows on average) 118, 157; 1000 (66 rows) 252, 217.
+// Few-row kernel against the other, 8 sequences of 2000 tokens, 32 heads over 8 of 128: 32 rows 27 us, 33;
+// 48 rows 34, 34; 64 rows 39, 34; 128 rows 63, 35.  One of 16000: 64 rows 40, 54; 128 rows 62, 55.  64 of 500,
+// 16 over 4 of 64: 48 rows 30, 29; 64 rows 38, 28; 96 rows 49, 29.  One prompt among 63 single tokens over 2048
+// tokens each: 256 queries (20 rows on average) 115, 133; 1000 (66 rows) 235, 171.
 static bool many_rows(int64_t n_tokens, int64_t batch, int64_t q_heads, int64_t kv_heads) {
   return n_tokens * (q_heads / kv_heads) >= 64 * batch;
 }

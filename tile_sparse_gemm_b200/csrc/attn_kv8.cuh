@@ -94,8 +94,8 @@ __device__ __forceinline__ int row_tiles(int m, int G) {
 
 // Shares are equal in units: a chunk is one, and a tile's own cost (its queries, its output) is
 // tile_units in front of its chunks: about half a chunk's time in a warp with 8 or 16 rows, 8000
-// cycles against a block's 2600 with 128 (four prompts of 100 to 512 tokens over up to 8000: 206 us with
-// one unit, 191 with four; 64 single tokens over up to 8000, 8 rows: 95 us with one, 101 with two).
+// cycles against a block's 2600 with 128 (four prompts of 100 to 512 tokens over up to 8000: 218 us with
+// one unit, 205 with two, 200 with four or six; 64 single tokens over up to 8000, 8 rows: 95 us with one, 101 with two).
 template <int R>
 constexpr int tile_units() {
   return R == 128 ? 4 : 1;

@@ -30,8 +30,9 @@
 // unit is raised.  A block with a smaller one takes bf16 instead, whose range holds every scale, on
 // the values' side, and its probabilities as sums of two numbers in two products.
 //
-// Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 329 us,
-// 713 TFLOP/s; 512 queries over 8000: 97 us, 670 TFLOP/s.  A block takes a CTA about 2600
+// Measured: 4 prompts of 1024 queries over 4000 tokens, 32 heads over 8 of 128: 325 us,
+// 722 TFLOP/s; 512 queries over 8000: 98 us, 663 TFLOP/s (value scales apart in every block,
+// each 2^-30 to 2^30: 696 and 201 us).  A block takes a CTA about 2600
 // cycles: the softmax warps' 1350 for exponentials and probabilities, 220 for the maximum,
 // 210 to exchange it, 390 to read and mask, and their waits; a tile costs 8000 more.
 // Work is shared out as in attn_kv8.cu: equal runs of blocks for all CTAs, wherever
@@ -174,7 +175,8 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // For a block whose value scales are apart, kept out of the loops that every block goes through: calls in them keep
 // the compiler from taking the next loads ahead, and products take a longer way (4 prompts of 1024 queries
-// over 4000 tokens: 366 us, 322 so).
+// over 4000 tokens: 366 us, 326 so).  The softmax warps, which wait for the scales anyway, do all of it: with
+// another wait in the warps that convert, 2048 queries of each of 4 prompts in fp16 take 336 us, 323 so.
 // A row's probabilities as sums of two bf16 numbers each, exactly: fp16 has 11 bits.
 template <int kCols>
 __device__ __noinline__ void split_probabilities(uint32_t s_at) {
@@ -193,29 +195,35 @@ __device__ __noinline__ void split_probabilities(uint32_t s_at) {
   }
 }
 
-// A lane's words of converted values in bf16, whose range holds them under every scale.
+// The converted values of a block in bf16, times their pages' scales, by the threads of the softmax.
 template <int CH, int D>
-__device__ __noinline__ void widen_values(uint8_t* v_at, const float2* scales, int w, int lane) {
-#pragma unroll 1
-  for (int i = 0; i < CH / 64 * (D / 64) * 16; ++i) {
-    const int atom = i / (D / 4), row = w * (D / 4) + i % (D / 4);
-    const float weight = scales[4 * atom + (lane >> 3)].y;
-    uint32_t* at = reinterpret_cast<uint32_t*>(v_at + atom * (D * 128) + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4);
+__device__ __noinline__ void widen_values(uint8_t* v_at, const float2* scales) {
+#pragma unroll 8
+  for (int i = threadIdx.x; i < CH * D / 2; i += 256) {
+    const int pair = i & 31, row = (i >> 5) % D, atom = (i >> 5) / D;  // two tokens, element, 64 tokens
+    const float weight = scales[4 * atom + (pair >> 3)].y;
+    uint32_t* at = reinterpret_cast<uint32_t*>(v_at + atom * (D * 128) + row * 128 + (((pair >> 2) ^ (row & 7)) << 4) + (pair & 3) * 4);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(at));
     *at = pack_bf16(f.x * weight, f.y * weight);
   }
+  tc::fence_proxy_async_smem();
 }
 
 // Both terms of the probabilities times the values.
 template <int CH, int R, int D>
 __device__ __noinline__ void products_apart(uint32_t o_at, uint32_t p_at, uint64_t v_desc, bool fresh) {
   constexpr int N = CH / 16;
-#pragma unroll 1
+#pragma unroll 16
   for (int i = 0; i < 2 * N; ++i) {
     const int k = i % N;
     mma_a_tmem(o_at, p_at + CH / 2 * (k / (N / 2)) + CH / 4 * (i / N) + 8 * (k % (N / 2)),
                v_desc + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), tc::idesc_bf16(R, D, false), !fresh || i > 0);
   }
+}
+
+// A slice of a page outside the pool, unless the slice lies before the window.
+__device__ __noinline__ void report_page(int32_t* status, int tok, int lo) {
+  if (tok + 16 > lo) set_status(status, PATCH_DEV_BOUNDS);
 }
 
 template <typename T, int D>
@@ -457,6 +465,8 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         if (unit < 0.0f) {
           split_probabilities<kCols>(s_at);
           tc::tmem_wait_st();
+          wait(v_full + (g & 1), g >> 1);
+          widen_values<CH, D>(smem + C::kV + (g & 1) * (CH * D * 2), scales + SL * (g & 7));
         }
         tc::tc_fence_before();
         __syncwarp();
@@ -616,8 +626,6 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
             *reinterpret_cast<uint32_t*>(dst + (4 * j + k) * 128 + (((lane >> 2) ^ ((4 * j + k) & 7)) << 4)) = e[k];
         }
       }
-      if (!__all_sync(0xFFFFFFFFu, wait(scales_full + (g & 7), g >> 3))) return false;
-      if (v_unit[g & 7] < 0.0f) widen_values<CH, D>(smem + C::kV + (g & 1) * (CH * D * 2), scales + SL * (g & 7), w, lane);
       dirty = (dirty & ~(1u << (g & 3))) | uint32_t(had != 0) << (g & 3);
       if (had) nan_block[g & 3] = g + 1;
       tc::fence_proxy_async_smem();
@@ -635,7 +643,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
   } else if (warp == 13) {
     // ================= loads: lane i < SL has the 16-token slice i of a block
     const uint32_t raw_k_at = tc::smem_u32(smem + C::kRawK), raw_v_at = tc::smem_u32(smem + C::kRawV);
-    int g = 0, keys = 0, values = 0;  // keys, values: blocks whose copies have been issued
+    int g = 0, ahead = 0;  // blocks whose copies have been issued; 1: the next one's keys as well
     bool ok = true;
     for (; ok && cur.c < cur.c_end; cur.next<CH, R>(a, G)) {
       const Tile& t = cur.t;
@@ -661,7 +669,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         const int n_box = max(min(CH >> P.box_shift, (t.hi - t0 + box - 1) >> P.box_shift), 0);
         const uint32_t bytes = uint32_t(n_box * D) << P.box_shift;
         const bool in = in_pool(phys), wanted = lane < SL && tok < t.hi;
-        if (wanted && !in && tok + 16 > t.lo) set_status(a.status, PATCH_DEV_BOUNDS);  // else before the window
+        if (wanted && !in) report_page(a.status, tok, t.lo);
         const int blk = in ? phys * a.kv_heads + t.h : int(a.n_pages) * a.kv_heads;  // behind the end: reads zeros
         const bool leads = wanted && (16 * lane & (box - 1)) == 0;
         auto issue = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
@@ -677,11 +685,10 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
         ok = g < 2 || wait(s_full + (g & 1), (g - 2) >> 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         issue(&P.k_map, raw_k_at + (g & 1) * C::kRawBytes, raw_k + (g & 1));
-        keys = g + 1;
         ok = g < 2 || wait(raw_v_free + (g & 1), (g - 2) >> 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        ahead = !__all_sync(0xFFFFFFFFu, ok);
+        if (ahead) break;
         issue(&P.v_map, raw_v_at + (g & 1) * C::kRawBytes, raw_v + (g & 1));
-        values = g + 1;
         // the largest value scale and the smallest but 0 (none is negative: their order is that of their bits)
         const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(sc.y)));
         const float least = __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(sc.y > 0.0f ? sc.y : INFINITY)));
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(RowsOf<T, D>::kThreads, 1) attn_kv8_rows_kerne
     // Let the copies in flight land: one of each ring place at most is not awaited yet.  After a timeout, this
     // warp's or another's, nobody else waits for them.
     for (int i = 1; i <= 2; ++i) {
-      const int k = keys - i, v = values - i;
+      const int k = g + ahead - i, v = g - i;
       if (k >= 0) tc::wait_bounded(raw_k + (k & 1), (k >> 1) & 1, abort_flag, tc::kDrainNs, a.status, true);
       if (v >= 0) tc::wait_bounded(raw_v + (v & 1), (v >> 1) & 1, abort_flag, tc::kDrainNs, a.status, true);
     }

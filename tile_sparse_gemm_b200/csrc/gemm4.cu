@@ -107,9 +107,9 @@ cudaError_t launch_quantize4(const void* W, int dtype, const patch_weight4& out,
 // each has its part of K (and of X), and their sums are added through distributed shared
 // memory, in the order of the parts.
 //
-// Measured: 128000 x 4096, 1 token, group 32: 69 us (codes and scales, 295 MB, at 4.3
+// Measured: 128000 x 4096, 1 token, group 32: 68 us (codes and scales, 295 MB, at 4.4
 // TB/s; fetching alone takes 46 us, the rest is what the integer and tensor instructions
-// of a block take beyond that); 14336 x 4096, 16 tokens: 23.5 us, of which 5 prepare X in
+// of a block take beyond that; 63 us in a row of launches); 14336 x 4096, 16 tokens: 23 us, of which 5 prepare X in
 // every CTA and 11 are the products; 4096 x 4096, 1 token: 5.0 us, mostly latency.
 namespace g4 {
 
@@ -187,7 +187,7 @@ __device__ __forceinline__ float load_of_cta(uint32_t addr, int rank) {  // the 
 }
 // S: type of the scales; NT: 8-token tiles; GS: log2 of the group; kParts: K is split over a cluster; kVec: K is a
 // multiple of kBlockK, so that a block's scales of a row are one aligned piece.  The last two are kernels of their own:
-// in a row of launches 128000 x 4096 takes 62 us, with kVec's checks in one kernel for both 64, with kParts' 66.
+// in a row of launches 128000 x 4096 takes 63 us, with kVec's checks in one kernel for both 64, with kParts' 66.
 template <typename S, int NT, int GS, bool kParts, bool kVec>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kernel(const __grid_constant__ Params P) {
   using C = Cfg<NT>;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) gemm4_kerne
                        : "memory");
         } else {
           const int left = row_groups - (kb0 + fet.b0 + fet.blk) * kGroups;
-          if (row_groups % 2 == 0) {  // rows of whole words: asynchronous as well, zeros behind K (29573 x 9600: 112 -> 93 us)
+          if (row_groups % 2 == 0) {  // rows of whole words: asynchronous as well, zeros behind K (29573 x 9600, 12 tokens: 112 -> 93 us)
 #pragma unroll
             for (int g = 0; g < kGroups; g += 2)
               asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst + g)),
@@ -541,10 +541,10 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
   // or 300 (two CTAs an SM), its sums 300, 1500 with each slice, or 2200 through the cluster.
   // Measured, two CTAs an SM and one: 128000 x 4096, group 128, 1 token 50 us, 58; 6 tokens 84, 65; 9000 x 11008,
   // group 32, 4 tokens 38, 25; where two do not fit, 8 tokens and group 32, 128000 x 4096 142 as two waves, 81.
-  // Measured with one part and with the chosen:
-  // 577 x 11072, 14 tokens 31 us, 12 (4 parts); 4096 x 14336, 8 tokens 39, 20 (8), 16 tokens 37, 25 (4); 256 x
-  // 14336, 1 token 12.3, 6.4 (8); 4096 x 4096, 1 token 7.1, 6.4 (2).  One part stays where the others lose: 4096 x
-  // 4096, 16 tokens 11.9, 12.3 with two; 14336 x 4096, 16 tokens 23, 28; 128000 x 4096, 1 token 66, 107.
+  // Measured in a row of launches with one part and with the chosen: 577 x 11072, 14 tokens 31 us, 12 (4 parts);
+  // 4096 x 14336, 8 tokens 26, 21, 16 tokens 38, 26; 256 x 14336, 1 token 12.1, 6.0 (8); 29573 x 9600, 12 tokens
+  // 93, 77 (2).  One part stays where the others lose, with two: 4096 x 4096, 1 token 6.0, 7.2, 16 tokens 11.9, 12.6;
+  // 14336 x 4096, 16 tokens 24, 28; 128000 x 4096, 1 token 63, 104.
   float best = 0.0f;
   int grid = 0;
   for (int ctas = C::kCtas; ctas >= 1; --ctas) {
