@@ -816,7 +816,9 @@ typedef struct {
  *   table, n_pos, rot_dim, layout  as patch_rope; table NULL (rot_dim 0): keys are stored as they are
  * A token whose page lies outside the block table or the pool, or whose
  * position lies outside the table, sets PATCH_DEV_BOUNDS; its page is not
- * written, keys or values.  So does past_lens[b] < 0 where there are new tokens, and none of these is stored.  dev_status may be NULL.  Two sequences must not append to one page.
+ * written, keys or values.  So does past_lens[b] < 0 where there are new tokens,
+ * and none of these is stored.  dev_status may be NULL.  Two sequences must not
+ * append to one page.
  * Errors: PATCH_ERR_INVALID_ARG (NULL, head counts, dtype, layout, n_tokens != batch
  * without cu_new), PATCH_ERR_SHAPE (page, head_dim, rot_dim not a multiple of 16 up to head_dim;
  * kv_heads > 65535, n_pages * kv_heads >= 2^31, n_tokens, max_pages or n_pos > 2^30, batch > 2^28),

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv8_kernel(const __grid_cons
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       // `up`: 2^x with amax in [2^x, 2^(x+1)), x from -126 to 126 so that 1 / up is normal as well; an infinity stays one
       const uint32_t ex = __float_as_uint(amax) >> 23, fit = min(max(ex, 1u), 253u);
-      const float down = ex == 255 ? 1.0f : __uint_as_float((254 - fit) << 23), up = ex == 255 ? 1.0f : __uint_as_float(fit << 23);
+      const float down = ex == 255 ? 1.0f : __uint_as_float((254 - fit) << 23);
+      const float up = ex == 255 ? 1.0f : __uint_as_float(fit << 23);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         qf[nt][s][0] = pack_f16(x[4 * s] * down, x[4 * s + 1] * down);

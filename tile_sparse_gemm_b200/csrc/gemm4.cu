@@ -551,7 +551,8 @@ static cudaError_t launch(Params P, int num_sms, cudaStream_t stream) {
     auto fits = [&](int x_blocks) {
       return x_blocks <= kMostBlocks && layout<NT, GS>(P.M, x_blocks).bytes <= kSmemOfSm / ctas - kSmemReserved;
     };
-    int slice = (P.blocks > kMostBlocks ? kMostBlocks : P.blocks - 1) / kKWarps * kKWarps;  // whole rounds of the warps, as many as fit
+    // of a slice: whole rounds of the warps, as many as fit
+    int slice = (P.blocks > kMostBlocks ? kMostBlocks : P.blocks - 1) / kKWarps * kKWarps;
     while (slice > 0 && !fits(slice)) slice -= kKWarps;
     for (int parts = 1; parts <= kMaxParts && parts <= P.blocks; parts *= 2) {
       const int local = (P.blocks + parts - 1) / parts;
